@@ -454,12 +454,10 @@ def run(s):
     how.update(causal=c["causal"], docs=s["docs"], prefix=s["prefix"])
     if kind == "weights":
         return fa.key_weights(s["q"], s["k"], s["lse"], **how)
+    o, lse = fa.fwd_scored(s["q"], s["k"], s["v"], **how)
     if kind == "fwd":
-        return fa.fwd_scored(s["q"], s["k"], s["v"], **how)
-    # a training step keeps what rounding takes off o for the gradient
-    lo = torch.empty_like(s["q"])
-    o, lse = fa.fwd_scored(s["q"], s["k"], s["v"], o_lo=lo, **how)
-    return (o, lse) + tuple(fa.bwd_scored(s["q"], s["k"], s["v"], o, s["do"], lse, o_lo=lo, **how))
+        return o, lse
+    return (o, lse) + tuple(fa.bwd_scored(s["q"], s["k"], s["v"], o, s["do"], lse, **how))
 
 
 # ------------------------------------------------------------------ exact --
