@@ -811,13 +811,14 @@ fa_status fa_fwd_scored(const void* q, const void* k, const void* v, void* o, vo
   p.wait_limit_ns = g_wait_limit_ns.load();
   if (sms <= 0) return FA_ERR_CUDA;
   const long long grid = items < sms ? items : sms;
+  // nothing changed and no rounding asked for: plain attention, fa_fwd_ex's bits
+  if (mod == fa::MOD_SCORED && p.sc.q_docs == nullptr && p.sc.prefix == nullptr && o_lo == nullptr)
+    return D == 128 ? launch_fwd<128, true, false, fa::MOD_SCORED>(mq, mk, mv, p, grid, st)
+                    : launch_fwd<64, true, false, fa::MOD_SCORED>(mq, mk, mv, p, grid, st);
   return with_mod(mod, [&](auto m) {
-    constexpr int MOD = decltype(m)::value, FINE = MOD | fa::MOD_FINE;
-    if (o_lo != nullptr)
-      return D == 128 ? launch_fwd<128, true, false, FINE>(mq, mk, mv, p, grid, st)
-                      : launch_fwd<64, true, false, FINE>(mq, mk, mv, p, grid, st);
-    return D == 128 ? launch_fwd<128, true, false, MOD>(mq, mk, mv, p, grid, st)
-                    : launch_fwd<64, true, false, MOD>(mq, mk, mv, p, grid, st);
+    constexpr int FINE = decltype(m)::value | fa::MOD_FINE;
+    return D == 128 ? launch_fwd<128, true, false, FINE>(mq, mk, mv, p, grid, st)
+                    : launch_fwd<64, true, false, FINE>(mq, mk, mv, p, grid, st);
   });
 }
 

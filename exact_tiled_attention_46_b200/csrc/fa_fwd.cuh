@@ -42,11 +42,15 @@
 // products, 29 of exponentials; what bounds all of them is the chain from one S
 // through P to the next on two warps per sub-partition.
 // MOD_FINE keeps P in two bf16 parts (the second takes the other half of S's
-// columns and a second set of P.V products) and writes, beside the bf16 O, what
-// its rounding took off: the gradient's Delta = dO.O subtracts from dP values
-// close to it, and a P or O rounded once to bf16 costs dq and dk half again of
-// what their own rounding does (train step B2 Hq16 Hkv4 L2048 D128, scores
-// peaked: relative error 2.7e-3 where the outputs' rounding alone gives 1.7e-3).
+// columns and a second set of P.V products), so that O is off by its own rounding
+// alone: relative error 1.66e-3 in bf16 where one part gives 1.9e-3, for 158 us
+// instead of 128 (cap, B4 H16 L2048 D128) and 901 instead of 661 (bias and prefix,
+// Hq32 Hkv8 L8191 D128).  Every scored call takes it but the one that changes
+// nothing, which is fa_fwd_ex bit for bit.  With o_lo it writes, beside the bf16 O,
+// what that rounding took off: the gradient's Delta = dO.O subtracts from dP
+// values close to it, and an O rounded to bf16 costs dq and dk half again of what
+// their own rounding does (train step B2 Hq16 Hkv4 L2048 D128, scores peaked:
+// relative error 2.8e-3 where the outputs' rounding alone gives 1.7e-3).
 #pragma once
 #include "sm100.cuh"
 #include "exp2_poly.cuh"
@@ -65,7 +69,7 @@ struct FwdParams {
   uint64_t wait_limit_ns;
   ScoreParams sc;          // scored variants only
   int item_rows;           // scored: query rows per item, 256 or 128 (no second query tile)
-  uint16_t* o_lo;          // MOD_FINE: [B, Lq, Hq, D] bf16, O minus its rounding
+  uint16_t* o_lo;          // MOD_FINE: [B, Lq, Hq, D] bf16, O minus its rounding, or nullptr
 };
 
 // FP8: Q, K, V are e4m3 (one byte per element) and both products run as
@@ -330,6 +334,7 @@ fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
            const __grid_constant__ CUtensorMap tm_v, const FwdParams p) {
   static_assert(!FP8 || D == 128, "the e4m3 path is built for D = 128");
   static_assert(MOD == MOD_NONE || (CAUSAL && !FP8), "the scored variants are bf16 and take the mask at run time");
+  static_assert(!(MOD & (MOD_CAP | MOD_BIAS)) || (MOD & MOD_FINE), "changed scores keep P in two parts");
   using C = FwdCfg<D, FP8, MOD>;
   constexpr int NS = C::NS;
   constexpr int KB = C::KB;                        // 128-byte column blocks per row
@@ -760,7 +765,7 @@ fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
           }
           const float msub = (m_used == -INFINITY) ? 0.f : m_used;
           const f2 nm = f2_pack(-msub, -msub);
-          f2 sum = f2_pack(0.f, 0.f);
+          f2 sum = f2_pack(0.f, 0.f), off2 = sum;                      // of p, and of what its two parts leave out
           float d0 = static_cast<float>(kb0 - pos);                    // distance key - query of the chunk's column 0
   #pragma unroll 1
           for (int qr = 0; qr < 4; ++qr) {
@@ -779,8 +784,7 @@ fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
             // GEN: with the mask and the bias' absolute value; EXACT: any argument
             auto chunk = [&](auto gen_c, auto exact_c) {
               constexpr bool GEN = decltype(gen_c)::value, EXACT = decltype(exact_c)::value;
-              uint32_t pk[16];
-              [[maybe_unused]] uint32_t pl[16];
+              uint32_t pk[16], pl[16];
               f2 dist = f2_pack(d0, d0 + 1.f);
   #pragma unroll
               for (int i = 0; i < 16; ++i) {
@@ -818,17 +822,15 @@ fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
                 }
                 pk[i] = pack_bf16x2(p0, p1);
                 sum = f2_add(sum, f2_pack(p0, p1));
-                if constexpr (FINE) {
-                  float r0, r1;
-                  resid_bf16x2(pk[i], p0, p1, r0, r1);
-                  pl[i] = pack_bf16x2(r0, r1);
-                } else {
-                  add_bf16x2_f32(lr0, lr1, pk[i]);
-                }
+                float r0, r1;
+                resid_bf16x2(pk[i], p0, p1, r0, r1);
+                pl[i] = pack_bf16x2(r0, r1);
+                resid_bf16x2(pl[i], r0, r1, r0, r1);
+                off2 = f2_add(off2, f2_pack(r0, r1));
               }
               // over this chunk's own columns of S: 16 of P, then 16 of its second part
               tmem_st_32x32b_x16(t_s + qr * 32, pk);
-              if constexpr (FINE) tmem_st_32x32b_x16(t_s + qr * 32 + 16, pl);
+              tmem_st_32x32b_x16(t_s + qr * 32 + 16, pl);
             };
             if (__any_sync(0xffffffffu, !(umax <= FA_TANH_LIMIT * FA_TANH_LIMIT))) chunk(std::true_type{}, std::true_type{});
             else if (masked || cross) chunk(std::true_type{}, std::false_type{});
@@ -836,7 +838,8 @@ fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
             d0 += 32.f;
           }
           f2_get(sum, ls0, ls1);
-          if constexpr (FINE) { lr0 = ls0; lr1 = ls1; }                // the parts' sum is the exact one
+          f2_get(off2, lr0, lr1);
+          lr0 = ls0 - lr0; lr1 = ls1 - lr1;
         } else {
         uint32_t sr[128];
         tmem_ld_32x32b_x128(t_s, sr);
@@ -873,14 +876,13 @@ fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
         // columns of S; ls = exact sum, lr = sum of the bf16 values (O's normaliser)
         auto exp_tile = [&](float msub, bool use_poly) {
           ls0 = ls1 = lr0 = lr1 = 0.f;
-          if constexpr (MOD != MOD_NONE && (BIAS || FINE)) {
+          if constexpr (FINE) {
             const f2 nm = f2_pack(-msub, -msub);
-            f2 sum = f2_pack(0.f, 0.f);
+            f2 sum = f2_pack(0.f, 0.f), off2 = sum;                    // of p, and of what its two parts leave out
             [[maybe_unused]] f2 dist = f2_pack(d0, d0 + 1.f);
   #pragma unroll
             for (int qr = 0; qr < 4; ++qr) {
-              uint32_t pk[16];
-              [[maybe_unused]] uint32_t pl[16];
+              uint32_t pk[16], pl[16];
   #pragma unroll
               for (int i = 0; i < 16; ++i) {
                 const int c = qr * 32 + 2 * i;
@@ -895,19 +897,18 @@ fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
                 p1 = ex2_approx(p1);
                 pk[i] = pack_bf16x2(p0, p1);
                 sum = f2_add(sum, f2_pack(p0, p1));
-                if constexpr (FINE) {
-                  float r0, r1;
-                  resid_bf16x2(pk[i], p0, p1, r0, r1);
-                  pl[i] = pack_bf16x2(r0, r1);
-                } else {
-                  add_bf16x2_f32(lr0, lr1, pk[i]);
-                }
+                float r0, r1;
+                resid_bf16x2(pk[i], p0, p1, r0, r1);
+                pl[i] = pack_bf16x2(r0, r1);
+                resid_bf16x2(pl[i], r0, r1, r0, r1);
+                off2 = f2_add(off2, f2_pack(r0, r1));
               }
               tmem_st_32x32b_x16(t_s + qr * 16, pk);
-              if constexpr (FINE) tmem_st_32x32b_x16(t_s + 64 + qr * 16, pl);
+              tmem_st_32x32b_x16(t_s + 64 + qr * 16, pl);
             }
             f2_get(sum, ls0, ls1);
-            if constexpr (FINE) { lr0 = ls0; lr1 = ls1; }              // the parts' sum is the exact one
+            f2_get(off2, lr0, lr1);
+            lr0 = ls0 - lr0; lr1 = ls1 - lr1;
           } else {
   #pragma unroll
           for (int half = 0; half < 2; ++half) {
@@ -1066,7 +1067,7 @@ fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
             wv.z = pack_bf16x2(__uint_as_float(ov[8 * i + 4]) * inv_l, __uint_as_float(ov[8 * i + 5]) * inv_l);
             wv.w = pack_bf16x2(__uint_as_float(ov[8 * i + 6]) * inv_l, __uint_as_float(ov[8 * i + 7]) * inv_l);
             dst[i] = wv;
-            if constexpr ((MOD & MOD_FINE) != 0) {
+            if (FINE && p.o_lo != nullptr) {
               const uint32_t hi[4] = {wv.x, wv.y, wv.z, wv.w};
               uint32_t lo[4];
 #pragma unroll

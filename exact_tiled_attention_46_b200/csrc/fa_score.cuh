@@ -27,7 +27,7 @@ struct ScoreParams {
   int* counter;            // work counter of the dynamic schedule, or nullptr; zeroed beside the tile facts
 };
 // Kernel variants: 0 the plain kernels, else SCORED plus what the scores need.
-// MOD_FINE (forward): P in two bf16 parts and O's rounding handed out.
+// MOD_FINE (forward): P in two bf16 parts, and O's rounding handed out when asked for.
 enum : int { MOD_NONE = 0, MOD_SCORED = 1, MOD_CAP = 2, MOD_BIAS = 4, MOD_FINE = 8 };
 constexpr float LOG2E = 1.4426950408889634f;
 

@@ -296,9 +296,10 @@ typedef struct {
  * Prefill forward over scored attention: fa_fwd_ex with the scores and masks of
  * *score (not NULL; all fields 0 or NULL: plain attention).  o_lo [B, Lq, Hq, D]
  * bf16 or NULL (only with o in FA_BF16): what o's rounding took off, so that
- * o + o_lo is O to about 16 bits; the probabilities then enter the product in
- * two bf16 parts.  For fa_bwd_scored, whose dq and dk lose precision to a
- * rounded O where few keys carry a row.  workspace: at least
+ * o + o_lo is O to about 16 bits.  For fa_bwd_scored, whose dq and dk lose
+ * precision to a rounded O where few keys carry a row.  The probabilities enter
+ * the product in two bf16 parts (16 bits), except where *score changes nothing
+ * and o_lo is NULL: that call gives fa_fwd_ex's bits.  workspace: at least
  * fa_scored_workspace_size(B, Lq, Lk) bytes, 16-byte aligned, used with
  * documents only (else it may be NULL).  Calls that share one workspace must be
  * ordered on one stream.
