@@ -15,7 +15,7 @@ Scores capped by a tanh or biased by distance, documents and prefixes, and a
 cache thinned by attention weight:
 
     o, lse = fwd_scored(q, k, v, causal=True, softcap=50.0, slopes=slopes, docs=doc_ids, prefix=prefix_lens)
-    dq, dk, dv = bwd_scored(q, k, v, o, do, lse, causal=True, softcap=50.0, slopes=slopes, docs=doc_ids)
+    dq, dk, dv = bwd_scored(q, k, v, o, do, lse, causal=True, softcap=50.0, slopes=slopes, docs=doc_ids, prefix=prefix_lens)
     w = key_weights(q, k, lse, causal=True, softcap=50.0)       # attention weight each key receives
     kept = cache_evict(k_cache, v_cache, w, seqlens, keep=1024, recent=128)
     o, lse = decode_scored(q, k_cache, v_cache, seqlens, k_new=k1, v_new=v1, softcap=50.0, weights=w)
@@ -459,7 +459,7 @@ def fwd_scored(q, k, v, scale: Optional[float] = None, causal: bool = False, sof
     docs int32 [B,L] or a pair ([B,Lq], [B,Lk]): only pairs of one document
     (negative: none); prefix int32 [B] (causal only): the first keys are seen by
     every query.  o_lo: a bf16 tensor like o that receives what o's rounding took
-    off, for bwd_scored (o in bf16 only).
+    off and spares bwd_scored forming O again (o in bf16 only).
     """
     B, Hq, Hkv, Lq, Lk, D = _qkv(q, k, v)
     if o_lo is not None:
@@ -486,7 +486,10 @@ def bwd_scored(q, k, v, o, do, lse, scale: Optional[float] = None, causal: bool 
                slopes: Optional[torch.Tensor] = None, docs=None, prefix: Optional[torch.Tensor] = None,
                grad_dtype=torch.bfloat16, o_lo: Optional[torch.Tensor] = None,
                workspace: Optional[torch.Tensor] = None):
-    """Backward of fwd_scored (same score arguments) from its o (and o_lo) and lse -> (dq, dk, dv)."""
+    """Backward of fwd_scored (same score arguments) from its o, o_lo and lse -> (dq, dk, dv).
+
+    Without o_lo the call forms O again, to 16 bits, which takes a forward's time.
+    """
     B, Hq, Hkv, Lq, Lk, D = _qkv(q, k, v)
     if o_lo is not None:
         _shape(o_lo, "o_lo", q.shape, torch.bfloat16, q.device)

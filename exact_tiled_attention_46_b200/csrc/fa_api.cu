@@ -361,6 +361,62 @@ fa_status launch_meta(fa::ScoreParams* sp, int B, int Lq, int Lk, void* ws, cuda
   return launch_status();
 }
 
+// Calls f with the variant as a constant.
+template <typename F>
+fa_status with_mod(int mod, F f) {
+  switch (mod) {
+    case fa::MOD_SCORED: return f(std::integral_constant<int, fa::MOD_SCORED>{});
+    case fa::MOD_SCORED | fa::MOD_CAP: return f(std::integral_constant<int, fa::MOD_SCORED | fa::MOD_CAP>{});
+    case fa::MOD_SCORED | fa::MOD_BIAS: return f(std::integral_constant<int, fa::MOD_SCORED | fa::MOD_BIAS>{});
+    default:
+      return f(std::integral_constant<int, fa::MOD_SCORED | fa::MOD_CAP | fa::MOD_BIAS>{});
+  }
+}
+
+// Query rows per item of the scored forward: two query tiles share an item's
+// keys and overlap each other's products and exponentials; a grid that would not
+// fill the SMs takes one.
+int fwd_item_rows(int B, int Hq, int Lq, int sms) {
+  return ((static_cast<long long>(Lq) + 255) / 256) * B * Hq < sms ? 128 : 256;
+}
+// (Query range, batch row, head) items of the scored forward.
+long long fwd_items(int B, int Hq, int Lq, int rows) {
+  return (static_cast<long long>(Lq) + rows - 1) / rows * B * Hq;
+}
+
+// The scored forward's launch, arguments checked and the documents' tile facts
+// in `sp`; `fine` asks for P in two parts even where nothing is changed.
+fa_status run_fwd_scored(const void* q, const void* k, const void* v, void* o, void* o_lo, float* lse, int B, int Hq,
+                         int Hkv, int Lq, int Lk, int D, float scale, const fa::ScoreParams& sp, int mod, bool fine,
+                         int o_dtype, int sms, cudaStream_t st) {
+  CUtensorMap mq, mk, mv;
+  if (!map_bshd(&mq, q, B, Lq, Hq, D, 64, 128, true) || !map_bshd(&mk, k, B, Lk, Hkv, D, 64, 128, true) ||
+      !map_bshd(&mv, v, B, Lk, Hkv, D, 64, 128, true))
+    return FA_ERR_CUDA;
+  fa::FwdParams p;
+  p.sc = sp;
+  p.item_rows = fwd_item_rows(B, Hq, Lq, sms);
+  const long long items = fwd_items(B, Hq, Lq, p.item_rows);
+  if (items <= sms) p.sc.counter = nullptr;       // one item per CTA: nothing to deal out
+  p.o = o; p.lse = lse; p.B = B; p.Hq = Hq; p.Hkv = Hkv; p.Lq = Lq; p.Lk = Lk;
+  p.o_lo = static_cast<uint16_t*>(o_lo);
+  p.num_pairs = (Lq + p.item_rows - 1) / p.item_rows;
+  p.scale_log2 = scale * fa::LOG2E;
+  p.o_scale = 1.f;
+  p.o_fp32 = (o_dtype == FA_FP32);
+  p.wait_limit_ns = g_wait_limit_ns.load();
+  const long long grid = items < sms ? items : sms;
+  // nothing changed and no rounding asked for: plain attention, fa_fwd_ex's bits
+  if (mod == fa::MOD_SCORED && sp.q_docs == nullptr && sp.prefix == nullptr && !fine)
+    return D == 128 ? launch_fwd<128, true, false, fa::MOD_SCORED>(mq, mk, mv, p, grid, st)
+                    : launch_fwd<64, true, false, fa::MOD_SCORED>(mq, mk, mv, p, grid, st);
+  return with_mod(mod, [&](auto m) {
+    constexpr int FINE = decltype(m)::value | fa::MOD_FINE;
+    return D == 128 ? launch_fwd<128, true, false, FINE>(mq, mk, mv, p, grid, st)
+                    : launch_fwd<64, true, false, FINE>(mq, mk, mv, p, grid, st);
+  });
+}
+
 // Parts into which fa_key_weights cuts the (query tile, head) pairs of a key
 // tile: enough items for six rounds of the SMs, which even out the causal
 // tiles' work, but no part shorter than eight pairs (two per warpgroup).  Parts
@@ -382,18 +438,6 @@ fa_status launch_kw(const CUtensorMap& mq, const CUtensorMap& mk, const fa::KwPa
   using C = fa::KwCfg<D>;
   if (!ensure_smem_attr(fa::kw_kernel<D, MOD>, C::SMEM_BYTES, attr_done)) return FA_ERR_CUDA;
   return launch_after(fa::kw_kernel<D, MOD>, dim3(grid), dim3(C::THREADS), C::SMEM_BYTES, st, mq, mk, p);
-}
-
-// Calls f with the variant as a constant.
-template <typename F>
-fa_status with_mod(int mod, F f) {
-  switch (mod) {
-    case fa::MOD_SCORED: return f(std::integral_constant<int, fa::MOD_SCORED>{});
-    case fa::MOD_SCORED | fa::MOD_CAP: return f(std::integral_constant<int, fa::MOD_SCORED | fa::MOD_CAP>{});
-    case fa::MOD_SCORED | fa::MOD_BIAS: return f(std::integral_constant<int, fa::MOD_SCORED | fa::MOD_BIAS>{});
-    default:
-      return f(std::integral_constant<int, fa::MOD_SCORED | fa::MOD_CAP | fa::MOD_BIAS>{});
-  }
 }
 
 // Keys per chunk of a scored decode: the longest of 1024, 512, 256, 128 that
@@ -433,11 +477,12 @@ fa_status run_bwd(const void* q, const void* k, const void* v, const void* o, co
   if (score != nullptr) {
     const fa_status s = score_params(score, scale, causal, Lq, Lk, &sp, &mod);
     if (s != FA_OK) return s;
-    if (B > 65535) return FA_ERR_UNSUPPORTED;
+    if (B > 65535 || !fits_int(fwd_items(B, Hq, Lq, 128))) return FA_ERR_UNSUPPORTED;
   }
   if (workspace_bytes < (score ? fa_bwd_scored_workspace_size(B, Hq, Lq, Lk, D) : fa_bwd_workspace_size(B, Hq, Lq, D)))
     return FA_ERR_INVALID_ARG;
   if (!fits_int(static_cast<long long>((Lk + 127) / 128) * B * Hkv)) return FA_ERR_UNSUPPORTED;
+  const int sms = sm_count();
   const size_t g_elt = grad_dtype == FA_FP32 ? 4 : 2;
   if (Lq == 0 || Lk == 0) {   // no (query, key) pair: the gradients that exist are zero
     const size_t nk = size_t(B) * Lk * Hkv * D * g_elt, nq = size_t(B) * Lq * Hq * D * g_elt;
@@ -469,8 +514,9 @@ fa_status run_bwd(const void* q, const void* k, const void* v, const void* o, co
       return FA_ERR_CUDA;
     fa::bwd_amax_kernel<<<dim3(amax_blocks, 4), 256, 0, st>>>(q_in, k_in, v_in, do_in, nq, nk, amax);
     if (launch_status() != FA_OK) return FA_ERR_CUDA;
-    fa::bwd_pre_kernel<false><<<pre_blocks, 256, 0, st>>>(static_cast<const uint16_t*>(o), nullptr, do_in, q_in, lse, amax,
-                                                          lse2, delta, q16, do16, B, Hq, Lq, lq_pad, D, nullptr);
+    fa::bwd_pre_kernel<false><<<pre_blocks, 256, 0, st>>>(static_cast<const uint16_t*>(o), nullptr, nullptr, do_in, q_in,
+                                                          lse, amax, lse2, delta, q16, do16, B, Hq, Lq, lq_pad, D,
+                                                          nullptr);
     if (launch_status() != FA_OK) return FA_ERR_CUDA;
   } else {
     // a chain of kernels that start while their predecessor ends; the first one
@@ -480,6 +526,17 @@ fa_status run_bwd(const void* q, const void* k, const void* v, const void* o, co
       if (cudaMemsetAsync(amax, 0, 32, st) != cudaSuccess) return FA_ERR_CUDA;
     } else if ((s = launch_meta(&sp, B, Lq, Lk, reinterpret_cast<char*>(amax) + 256, st, amax)) != FA_OK) {
       return s;
+    }
+    // without what rounding took off o, O is formed again, in two bf16 parts that
+    // lie where bwd_pre_kernel puts q16 and do16 (each chunk is read by the thread
+    // that then writes it): 83 us of 537 for the training step B2 Hq16 Hkv4 L2048 D128 with a cap
+    const uint16_t *lo = static_cast<const uint16_t*>(o_lo), *o_new = nullptr;
+    if (lo == nullptr) {
+      if (sms <= 0) return FA_ERR_CUDA;
+      s = run_fwd_scored(q, k, v, q16, do16, nullptr, B, Hq, Hkv, Lq, Lk, D, scale, sp, mod, true, FA_BF16, sms, st);
+      if (s != FA_OK) return s;
+      o_new = q16;
+      lo = do16;
     }
     // every row counts unless documents, or more queries than keys under the
     // causal mask, leave some without a key
@@ -491,8 +548,8 @@ fa_status run_bwd(const void* q, const void* k, const void* v, const void* o, co
       s = launch_after(fa::bwd_amax_kernel, dim3(amax_blocks, 4), dim3(256), 0, st, q_in, k_in, v_in, do_in, nq, nk, amax);
     }
     if (s != FA_OK) return s;
-    s = launch_after(fa::bwd_pre_kernel<true>, dim3(pre_blocks), dim3(256), 0, st, static_cast<const uint16_t*>(o),
-                     static_cast<const uint16_t*>(o_lo), do_in, q_in, lse, static_cast<const uint32_t*>(amax), lse2, delta,
+    s = launch_after(fa::bwd_pre_kernel<true>, dim3(pre_blocks), dim3(256), 0, st, static_cast<const uint16_t*>(o), o_new,
+                     lo, do_in, q_in, lse, static_cast<const uint32_t*>(amax), lse2, delta,
                      q16, do16, B, Hq, Lq, lq_pad, D, dq_acc);
     if (s != FA_OK) return s;
   }
@@ -513,7 +570,6 @@ fa_status run_bwd(const void* q, const void* k, const void* v, const void* o, co
   p.num_items = static_cast<int>(((Lk + 127) / 128) * B * Hkv);
   p.work_counter = counter;
   p.sc = sp;
-  const int sms = sm_count();
   if (sms <= 0) return FA_ERR_CUDA;
   const unsigned grid = static_cast<unsigned>(std::min(p.num_items, sms));
   fa_status s;
@@ -775,17 +831,14 @@ fa_status fa_fwd_scored(const void* q, const void* k, const void* v, void* o, vo
     return FA_ERR_INVALID_ARG;
   if (o_lo != nullptr && o_dtype != FA_BF16) return FA_ERR_INVALID_ARG;
   if (D != 64 && D != 128) return FA_ERR_UNSUPPORTED;
-  fa::FwdParams p;
+  fa::ScoreParams sp{};
   int mod = fa::MOD_NONE;
-  fa_status s = score_params(score, scale, causal, Lq, Lk, &p.sc, &mod);
+  fa_status s = score_params(score, scale, causal, Lq, Lk, &sp, &mod);
   if (s != FA_OK) return s;
   const int sms = sm_count();
-  // two query tiles per item share its keys and overlap each other's products
-  // and exponentials; a grid that would not fill the SMs takes one
-  p.item_rows = ((static_cast<long long>(Lq) + 255) / 256) * B * Hq < sms ? 128 : 256;
-  const long long pairs = (static_cast<long long>(Lq) + p.item_rows - 1) / p.item_rows;
-  const long long items = pairs * B * Hq;
-  if (!fits_int(items) || !fits_int(static_cast<long long>(B) * Hq) || B > 65535) return FA_ERR_UNSUPPORTED;
+  if (!fits_int(fwd_items(B, Hq, Lq, fwd_item_rows(B, Hq, Lq, sms))) || !fits_int(static_cast<long long>(B) * Hq) ||
+      B > 65535)
+    return FA_ERR_UNSUPPORTED;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (Lq == 0) return FA_OK;
   if (Lk == 0) {
@@ -794,32 +847,11 @@ fa_status fa_fwd_scored(const void* q, const void* k, const void* v, void* o, vo
     if (o_lo != nullptr) fill_empty_rows_kernel<<<296, 256, 0, st>>>(o_lo, nullptr, n_o, 0, 0);
     return launch_status();
   }
-  if (p.sc.q_docs != nullptr && (!workspace || workspace_bytes < fa_scored_workspace_size(B, Lq, Lk)))
+  if (sp.q_docs != nullptr && (!workspace || workspace_bytes < fa_scored_workspace_size(B, Lq, Lk)))
     return FA_ERR_INVALID_ARG;
-  CUtensorMap mq, mk, mv;
-  if (!map_bshd(&mq, q, B, Lq, Hq, D, 64, 128, true) || !map_bshd(&mk, k, B, Lk, Hkv, D, 64, 128, true) ||
-      !map_bshd(&mv, v, B, Lk, Hkv, D, 64, 128, true))
-    return FA_ERR_CUDA;
-  if ((s = launch_meta(&p.sc, B, Lq, Lk, workspace, st)) != FA_OK) return s;
-  if (items <= sms) p.sc.counter = nullptr;       // one item per CTA: nothing to deal out
-  p.o = o; p.lse = lse; p.B = B; p.Hq = Hq; p.Hkv = Hkv; p.Lq = Lq; p.Lk = Lk;
-  p.o_lo = static_cast<uint16_t*>(o_lo);
-  p.num_pairs = static_cast<int>(pairs);
-  p.scale_log2 = scale * fa::LOG2E;
-  p.o_scale = 1.f;
-  p.o_fp32 = (o_dtype == FA_FP32);
-  p.wait_limit_ns = g_wait_limit_ns.load();
   if (sms <= 0) return FA_ERR_CUDA;
-  const long long grid = items < sms ? items : sms;
-  // nothing changed and no rounding asked for: plain attention, fa_fwd_ex's bits
-  if (mod == fa::MOD_SCORED && p.sc.q_docs == nullptr && p.sc.prefix == nullptr && o_lo == nullptr)
-    return D == 128 ? launch_fwd<128, true, false, fa::MOD_SCORED>(mq, mk, mv, p, grid, st)
-                    : launch_fwd<64, true, false, fa::MOD_SCORED>(mq, mk, mv, p, grid, st);
-  return with_mod(mod, [&](auto m) {
-    constexpr int FINE = decltype(m)::value | fa::MOD_FINE;
-    return D == 128 ? launch_fwd<128, true, false, FINE>(mq, mk, mv, p, grid, st)
-                    : launch_fwd<64, true, false, FINE>(mq, mk, mv, p, grid, st);
-  });
+  if ((s = launch_meta(&sp, B, Lq, Lk, workspace, st)) != FA_OK) return s;
+  return run_fwd_scored(q, k, v, o, o_lo, lse, B, Hq, Hkv, Lq, Lk, D, scale, sp, mod, o_lo != nullptr, o_dtype, sms, st);
 }
 
 size_t fa_bwd_scored_workspace_size(int B, int Hq, int Lq, int Lk, int D) {

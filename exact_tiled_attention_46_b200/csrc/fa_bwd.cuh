@@ -307,9 +307,13 @@ __global__ void __launch_bounds__(256) bwd_amax_scored_kernel(const uint16_t* q,
 // of the dP^T products.  One thread per 8-element chunk of a (b, i, h) row,
 // h fastest, so that a warp reads and writes contiguous memory; the D / 8
 // threads of a row sum Delta with shuffles.  SCORED: rows that see no key
-// (lse = -inf) become zeros; o_lo (or nullptr) is what o's rounding took off.
+// (lse = -inf) become zeros; o_lo is what o's rounding took off.  With o_new,
+// o_new + o_lo is O formed again, and o_lo holds for an element of o that is its
+// rounding: one further off (the o of a call over more keys than this one's) is
+// taken as it is.  q16 may be o_new, and do16 o_lo.
 template <bool SCORED>
-__global__ void __launch_bounds__(256) bwd_pre_kernel(const uint16_t* o, const uint16_t* o_lo, const uint16_t* dO,
+__global__ void __launch_bounds__(256) bwd_pre_kernel(const uint16_t* o, const uint16_t* o_new, const uint16_t* o_lo,
+                                                      const uint16_t* dO,
                                                       const uint16_t* q,
                                                       const float* lse, const uint32_t* amax, float* lse2,
                                                       float* delta, uint16_t* q16, uint16_t* do16, int B, int Hq,
@@ -333,21 +337,29 @@ __global__ void __launch_bounds__(256) bwd_pre_kernel(const uint16_t* o, const u
       uint4 a = reinterpret_cast<const uint4*>(o)[off];
       uint4 g = reinterpret_cast<const uint4*>(dO)[off];
       uint4 x = reinterpret_cast<const uint4*>(q)[off];
-      uint4 al = make_uint4(0u, 0u, 0u, 0u);
-      if (SCORED && o_lo != nullptr) al = reinterpret_cast<const uint4*>(o_lo)[off];
+      uint4 al = make_uint4(0u, 0u, 0u, 0u), an = a;
+      if (SCORED) al = reinterpret_cast<const uint4*>(o_lo)[off];
+      if (SCORED && o_new != nullptr) an = reinterpret_cast<const uint4*>(o_new)[off];
       if (SCORED && lse[(size_t(b) * Hq + h) * Lq + i] == -INFINITY) a = al = g = x = make_uint4(0u, 0u, 0u, 0u);
-      [[maybe_unused]] const uint32_t alv[4] = {al.x, al.y, al.z, al.w};
+      [[maybe_unused]] const uint32_t alv[4] = {al.x, al.y, al.z, al.w}, anv[4] = {an.x, an.y, an.z, an.w};
+      // O of one element: a's rounding undone where a is the rounding of n + l
+      // (half a step of bf16, and l's own)
+      [[maybe_unused]] auto whole = [](float a, float n, float l) {
+        const float x = n + l;
+        return fabsf(x - a) <= 0x1.01p-8f * fabsf(x) ? x : a;
+      };
       const uint32_t av[4] = {a.x, a.y, a.z, a.w}, gv[4] = {g.x, g.y, g.z, g.w}, xv[4] = {x.x, x.y, x.z, x.w};
       uint32_t hq[4], hd[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const float g0 = __uint_as_float(gv[e] << 16), g1 = __uint_as_float(gv[e] & 0xffff0000u);
-        acc = fmaf(__uint_as_float(av[e] << 16), g0, acc);
-        acc = fmaf(__uint_as_float(av[e] & 0xffff0000u), g1, acc);
+        float a0 = __uint_as_float(av[e] << 16), a1 = __uint_as_float(av[e] & 0xffff0000u);
         if constexpr (SCORED) {
-          acc = fmaf(__uint_as_float(alv[e] << 16), g0, acc);
-          acc = fmaf(__uint_as_float(alv[e] & 0xffff0000u), g1, acc);
+          a0 = whole(a0, __uint_as_float(anv[e] << 16), __uint_as_float(alv[e] << 16));
+          a1 = whole(a1, __uint_as_float(anv[e] & 0xffff0000u), __uint_as_float(alv[e] & 0xffff0000u));
         }
+        acc = fmaf(a0, g0, acc);
+        acc = fmaf(a1, g1, acc);
         hd[e] = pack_f16x2(g0 * fdo, g1 * fdo);
         hq[e] = pack_f16x2(__uint_as_float(xv[e] << 16) * fq, __uint_as_float(xv[e] & 0xffff0000u) * fq);
       }

@@ -312,7 +312,9 @@ fa_status fa_fwd_scored(const void* q, const void* k, const void* v, void* o, vo
 
 /*
  * Its gradient: fa_bwd with the same *score as the forward that wrote o, o_lo
- * (or NULL) and lse.
+ * and lse.  Without o_lo (NULL) the call forms O to 16 bits again (a forward's
+ * time more) and corrects every element of o that is its rounding; an o of other
+ * keys (a part of a context, under its whole log-sums) is taken as it is.
  * The tanh's derivative is part of dq and dk.  An inf or NaN in an allowed pair
  * gives non-finite gradients.  workspace: at least
  * fa_bwd_scored_workspace_size() bytes, 256-byte aligned.

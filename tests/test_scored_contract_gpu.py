@@ -40,3 +40,36 @@ def test_forward_keeps_sixteen_bits_of_p(name):
         O, lim = S.o_bound(P, V, err, fine=True)
         S.check(f64(o)[b, :, h], O, lim, f"O[{b},:,{h}]", 2.0 ** -23)
     assert torch.equal(forward(p)[0], o.to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("name", CHANGED)
+def test_backward_undoes_the_rounding_of_o(name):
+    """The gradient without o_lo is that of O to 16 bits: the bits of the call with o_lo, inside the bound of two parts."""
+    p = problem(name, seed=7)
+    lo = torch.empty_like(p.q).cuda()
+    o, lse = forward(p, o_lo=lo)
+    args = (*cuda(p, "q", "k", "v"), o, p.do.cuda(), lse)
+    grads = fa.bwd_scored(*args, grad_dtype=torch.float32, **p.how("cuda"))
+    S.check_bwd(p, *grads, bf16_output=False, fine=True)
+    given = fa.bwd_scored(*args, o_lo=lo, grad_dtype=torch.float32, **p.how("cuda"))
+    assert torch.equal(grads[1], given[1]) and torch.equal(grads[2], given[2])       # dQ is summed in any order
+
+
+def test_backward_of_a_part_of_the_context_takes_o_as_it_is():
+    """O and log-sums of all keys beside a part of them: where o is no rounding of the part's own O, Delta is o's."""
+    p = S.Problem(1, 4, 2, 200, 400, 64, causal=False, cap=8.0, seed=12)
+    q, k, v, do = cuda(p, "q", "k", "v", "do")
+    o, lse = forward(p)
+    for part in (slice(0, 256), slice(256, 400)):
+        ks, vs = k[:, part].contiguous(), v[:, part].contiguous()
+        got = fa.bwd_scored(q, ks, vs, o, do, lse, grad_dtype=torch.float32, **p.how("cuda"))
+        ref = fa.bwd_scored(q, ks, vs, o, do, lse, o_lo=torch.zeros_like(o), grad_dtype=torch.float32, **p.how("cuda"))
+        assert torch.equal(got[2], ref[2])
+        # an element that happens to round to o all the same moves Delta by half a step of its own at most
+        for b, h, g, P, l, d, ok, Q, K, V, dO, err in p.heads():
+            delta = BF * np.sum(np.abs(dO * (P @ V)), axis=1, keepdims=True) * (1 + 2.0 ** -6)
+            Pp, dp, Kp = P[:, part], d[:, part], np.abs(K[part])
+            # fp16's half step of dS twice, and fp32 sums
+            dS = np.abs(Pp * (dO @ V[part].T - np.sum(dO * (P @ V), axis=1, keepdims=True)) * dp)
+            lim = p.scale * (delta * (Pp * dp) + 2 * S.FP16 * (dS + delta * Pp) + 2.0 ** -20) @ Kp
+            assert (np.abs(f64(got[0] - ref[0])[b, :, h]) <= lim).all()
