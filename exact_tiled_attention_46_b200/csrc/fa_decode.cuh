@@ -587,9 +587,11 @@ decode_split_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
       const size_t prow = (static_cast<size_t>(b) * p.Hq + hq0 + h2) * p.max_splits + I.split;
       if (!index_ok(prow, 1, static_cast<size_t>(p.B) * p.Hq * p.max_splits, W_IDX_DEC_PART)) continue;
       // O is normalised by the sum of the rounded p that the products used, the
-      // LSE by the exact sum
-      p.o_part[prow * D + d] = LR > 0.f ? O / LR : 0.f;
-      if (d == 0) p.lse_part[prow] = L > 0.f ? (mx + log2f(L)) * LN2 : -INFINITY;
+      // LSE by the exact sum.  SCORED: a NaN among the scores makes both NaN (only
+      // a sum of 0 means that nothing was attended)
+      const bool some = SCORED ? L != 0.f : L > 0.f, some_r = SCORED ? LR != 0.f : LR > 0.f;
+      p.o_part[prow * D + d] = some_r ? O / LR : 0.f;
+      if (d == 0) p.lse_part[prow] = some ? (mx + log2f(L)) * LN2 : -INFINITY;
     }
 
     // APPEND: the first head group of each kv head writes the new rows into the

@@ -343,7 +343,9 @@ fa_status fa_bwd_scored(const void* q, const void* k, const void* v, const void*
  *            depend on timing.
  * A page-table entry outside the pool reads as zero rows and is reported by
  * fa_device_status(), as is an append without room (o = 0, lse = -inf, nothing
- * written).  Any number of query heads per kv head.  workspace: at least
+ * written).  A NaN among a head's attended scores (a NaN in q or an attended key,
+ * an infinite score without a cap) gives it o = NaN and lse = NaN, and NaN weights
+ * to the rows that its kv head attends.  Any number of query heads per kv head.  workspace: at least
  * fa_decode_scored_workspace_size(B, Hq, Hkv, rows, D, weights != NULL) bytes,
  * where rows = page_size * pages_per_seq + (append ? 1 : 0), 256-byte aligned.
  * Calls that share one workspace must be ordered on one stream.

@@ -10,7 +10,7 @@ import exact_tiled_attention_46_b200 as fa
 import scored as S
 from parity import need_gpu
 from scored import BF, f64
-from test_scored_gpu import CASES, cuda, forward, problem
+from test_scored_gpu import CASES, cuda, decode_problem, forward, problem
 
 pytestmark = pytest.mark.gpu
 
@@ -73,3 +73,39 @@ def test_backward_of_a_part_of_the_context_takes_o_as_it_is():
             dS = np.abs(Pp * (dO @ V[part].T - np.sum(dO * (P @ V), axis=1, keepdims=True)) * dp)
             lim = p.scale * (delta * (Pp * dp) + 2 * S.FP16 * (dS + delta * Pp) + 2.0 ** -20) @ Kp
             assert (np.abs(f64(got[0] - ref[0])[b, :, h]) <= lim).all()
+
+
+# ----------------------------------------------------------------- decode --
+@pytest.mark.parametrize("rows,bad,cap,append", [(90, 40, 0.0, False), (90, 0, 5.0, True), (900, 500, 5.0, True),
+                                                 (900, 899, 0.0, False), (5000, 3, 0.0, True), (5000, 4999, 9.0, False)])
+@pytest.mark.parametrize("value", (math.nan, math.inf))
+def test_decode_shows_a_nan_score(rows, bad, cap, append, value):
+    """A key whose score is no number makes its heads' results NaN and touches no other head or sequence."""
+    q, k, v, args, _, _ = decode_problem(2, 6, 3, 64, [rows, rows], rows + 1, cap=cap, append=append, seed=rows)
+    w0 = args["weights"].clone()
+    o, lse = fa.decode_scored(q, k, v, **args)
+    w = args["weights"].clone()
+    args["weights"].copy_(w0)
+    # an infinite score without a cap is one as well (inf - inf); with a cap it is the cap
+    k[1, bad, 2] = 0.0
+    k[1, bad, 2, 5] = value
+    q[1, 4:, 5] = 1.0
+    o2, lse2 = fa.decode_scored(q, k, v, **args)
+    w2 = args["weights"]
+    n = rows + (1 if append else 0)
+    assert torch.equal(o2[0], o[0]) and torch.equal(o2[1, :4], o[1, :4]) and torch.equal(lse2[1, :4], lse[1, :4])
+    assert torch.equal(w2[0], w[0]) and torch.equal(w2[1, :2], w[1, :2]) and torch.equal(w2[1, 2, n:], w0[1, 2, n:])
+    if cap and value == math.inf:
+        assert torch.isfinite(o2).all() and torch.isfinite(lse2).all() and torch.isfinite(w2).all()
+    else:
+        assert torch.isnan(o2[1, 4:]).all() and torch.isnan(lse2[1, 4:]).all() and torch.isnan(w2[1, 2, :n]).all()
+
+
+def test_decode_shows_a_nan_query():
+    q, k, v, args, _, _ = decode_problem(2, 4, 2, 128, [300, 0], 300, seed=2)
+    q[:, 1, 7] = math.nan
+    w0 = args["weights"].clone()
+    o, lse = fa.decode_scored(q, k, v, **args)
+    assert torch.isnan(o[0, 1]).all() and torch.isnan(lse[0, 1]) and torch.isfinite(o[0, [0, 2, 3]]).all()
+    assert torch.isnan(args["weights"][0, 0, :300]).all() and torch.isfinite(args["weights"][0, 1]).all()
+    assert torch.isneginf(lse[1]).all() and not o[1].any() and torch.equal(args["weights"][1], w0[1])
