@@ -210,11 +210,8 @@ __device__ __forceinline__ DecItem dec_item(const DecParams& p, int HG, int GPK,
 __device__ __forceinline__ void dec_score(const DecParams& p, float slope2, float back, float& s0, float& s1) {
   if (p.cap_log2 > 0.f) {
     const float y0 = s0 * p.y_scale, y1 = s1 * p.y_scale;
-    if (__any_sync(0xffffffffu, !(fmaxf(fabsf(y0), fabsf(y1)) <= FA_TANH_LIMIT))) {
-      s0 = tanh_mufu(y0); s1 = tanh_mufu(y1);
-    } else {
-      tanh_poly2(y0, y1, s0, s1);
-    }
+    if (__any_sync(0xffffffffu, !(fmaxf(fabsf(y0), fabsf(y1)) <= FA_TANH_LIMIT))) tanh_any2(y0, y1, s0, s1);
+    else tanh_poly2(y0, y1, s0, s1);
     s0 *= p.cap_log2; s1 *= p.cap_log2;
   } else {
     s0 *= p.scale_log2; s1 *= p.scale_log2;

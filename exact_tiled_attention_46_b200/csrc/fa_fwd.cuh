@@ -781,7 +781,7 @@ fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
               f2_get(f2_mul(y[i], y[i]), u0, u1);
               umax = fmax3(umax, u0, u1);
             }
-            // GEN: with the mask and the bias' absolute value; EXACT: any argument
+            // GEN: with the mask and the bias' absolute value; EXACT: arguments past FA_TANH_LIMIT too
             auto chunk = [&](auto gen_c, auto exact_c) {
               constexpr bool GEN = decltype(gen_c)::value, EXACT = decltype(exact_c)::value;
               uint32_t pk[16], pl[16];
@@ -799,18 +799,21 @@ fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
                   b = f2_fma(d, cslope, nm);
                   dist = f2_add(dist, ctwo);
                 }
-                if constexpr (EXACT) {
-                  float y0, y1;
+                const f2 u = f2_mul(y[i], y[i]);
+                f2 q = f2_fma(u, ck5, ck4);
+                q = f2_fma(q, u, ck3);
+                q = f2_fma(q, u, ck2);
+                q = f2_fma(q, u, ck1);
+                q = f2_fma(q, u, ck0);
+                x = f2_fma(y[i], q, b);
+                if constexpr (EXACT) {                                 // each argument by itself: fa_score.cuh
+                  float y0, y1, u0, u1, x0, x1, e0, e1;
                   f2_get(y[i], y0, y1);
-                  x = f2_fma(f2_pack(tanh_mufu(y0), tanh_mufu(y1)), f2_pack(cap2, cap2), b);
-                } else {
-                  const f2 u = f2_mul(y[i], y[i]);
-                  f2 q = f2_fma(u, ck5, ck4);
-                  q = f2_fma(q, u, ck3);
-                  q = f2_fma(q, u, ck2);
-                  q = f2_fma(q, u, ck1);
-                  q = f2_fma(q, u, ck0);
-                  x = f2_fma(y[i], q, b);
+                  f2_get(u, u0, u1);
+                  f2_get(x, x0, x1);
+                  f2_get(f2_fma(f2_pack(tanh_mufu(y0), tanh_mufu(y1)), f2_pack(cap2, cap2), b), e0, e1);
+                  constexpr float L2 = FA_TANH_LIMIT * FA_TANH_LIMIT;
+                  x = f2_pack(u0 <= L2 ? x0 : e0, u1 <= L2 ? x1 : e1);
                 }
                 float p0, p1;
                 f2_get(x, p0, p1);
@@ -973,12 +976,14 @@ fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
           }
         } else {
         bool slow = __any_sync(0xffffffffu, m_used == -INFINITY);
+        [[maybe_unused]] bool over = true;           // this row's own P against its reference is too large, or not known
         if (!slow) {
           // the branch keeps the polynomial loop and the all-MUFU loop apart, so
           // that the compiler cannot evaluate both and select
           if (need_mask) exp_tile(m_used, false);
           else exp_tile(m_used, true);
-          slow = __any_sync(0xffffffffu, !(ls0 + ls1 <= FWD_FAST_LIMIT));
+          over = !(ls0 + ls1 <= FWD_FAST_LIMIT);
+          slow = __any_sync(0xffffffffu, over);
         }
         if (slow) {
           float mx0 = s[0], mx1 = s[1], mx2 = s[2], mx3 = s[3];
@@ -999,7 +1004,9 @@ fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
           }
           }
           const float m_tile = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)) * (BIAS ? 1.f : sl2);
-          const bool resc = m_tile > m_used + FWD_TAU;   // false while both are -inf
+          // scored: a row that could have kept its reference keeps it, whatever the
+          // warp's other rows ran into
+          const bool resc = m_tile > m_used + FWD_TAU && (MOD == MOD_NONE || over);   // false while both are -inf
           float alpha = 1.f;
           if (resc) { alpha = ex2_approx(m_used - m_tile); l *= alpha; lr *= alpha; m_used = m_tile; }
           if (j > st && __any_sync(0xffffffffu, resc)) {
@@ -1018,6 +1025,9 @@ fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
         }
         l += ls0 + ls1;
         lr += lr0 + lr1;
+        // a row of NaN scores has no maximum; any reference does, and the warp's
+        // other rows keep to their own
+        if (MOD != MOD_NONE && l != l && m_used == -INFINITY) m_used = 0.f;
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive(&p_full[t]);

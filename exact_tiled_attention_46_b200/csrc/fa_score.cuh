@@ -133,8 +133,11 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return y;
 }
 // tanh for any argument on the MUFU unit: 1 - 2 / (1 + e^(2y)), absolute error
-// about 2^-22 (two MUFU operations; the kernels use it for tiles that hold an
-// argument beyond 1, and the polynomial below otherwise).
+// about 2^-22 (two MUFU operations).  The kernels take it for arguments beyond
+// FA_TANH_LIMIT, where that is half a step of fp32 relative to the value, and the
+// polynomial below within.  Each argument decides for itself: what else stands in
+// the tile, masked or of another row, changes no bit of a score.  (A warp without
+// any argument beyond the limit skips the MUFU form.)
 __device__ __forceinline__ float tanh_mufu(float y) {
   return fmaf(-2.f, rcp_approx(1.f + ex2_approx(2.f * LOG2E * y)), 1.f);
 }
@@ -149,10 +152,15 @@ __device__ __forceinline__ void tanh_poly2(float y0, float y1, float& t0, float&
   ffma2(p0, p1, p0, p1, u0, u1, FA_TANH_C0, FA_TANH_C0);
   ffma2(t0, t1, y0, y1, p0, p1, 0.f, 0.f);
 }
+// tanh of any two arguments (a NaN gives a NaN).
+__device__ __forceinline__ void tanh_any2(float y0, float y1, float& t0, float& t1) {
+  tanh_poly2(y0, y1, t0, t1);
+  t0 = fabsf(y0) <= FA_TANH_LIMIT ? t0 : tanh_mufu(y0);
+  t1 = fabsf(y1) <= FA_TANH_LIMIT ? t1 : tanh_mufu(y1);
+}
 
-// Raw products x[0..16) to t = tanh(x * y_scale), in place.  The polynomial form
-// is taken when no argument of the warp's columns passes FA_TANH_LIMIT: it costs
-// 8 packed FMAs per pair where the general form costs 4 MUFU operations.
+// Raw products x[0..16) to t = tanh(x * y_scale), in place.  The polynomial costs
+// 8 packed FMAs per pair, the other form 4 MUFU operations besides.
 __device__ __forceinline__ void cap_tile(float (&x)[16], float ysc) {
   float a0 = 0.f, a1 = 0.f;
 #pragma unroll
@@ -160,7 +168,7 @@ __device__ __forceinline__ void cap_tile(float (&x)[16], float ysc) {
     a0 = fmaxf(a0, fmaxf(fabsf(x[c]), fabsf(x[c + 1])));
     a1 = fmaxf(a1, fmaxf(fabsf(x[c + 2]), fabsf(x[c + 3])));
   }
-  if (!__any_sync(0xffffffffu, fmaxf(a0, a1) * ysc > FA_TANH_LIMIT)) {
+  if (!__any_sync(0xffffffffu, !(fmaxf(a0, a1) * ysc <= FA_TANH_LIMIT))) {
 #pragma unroll
     for (int c = 0; c < 16; c += 2) {
       float y0, y1;
@@ -169,7 +177,11 @@ __device__ __forceinline__ void cap_tile(float (&x)[16], float ysc) {
     }
   } else {
 #pragma unroll
-    for (int c = 0; c < 16; ++c) x[c] = tanh_mufu(x[c] * ysc);
+    for (int c = 0; c < 16; c += 2) {
+      float y0, y1;
+      ffma2(y0, y1, x[c], x[c + 1], ysc, ysc, 0.f, 0.f);
+      tanh_any2(y0, y1, x[c], x[c + 1]);
+    }
   }
 }
 

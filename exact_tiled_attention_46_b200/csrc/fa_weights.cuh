@@ -359,8 +359,8 @@ kw_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
           const int w4 = c4 * CW >> 5;
           const uint32_t bits = (w4 == 0 ? m[0] : w4 == 1 ? m[1] : w4 == 2 ? m[2] : m[3]) >> (c4 * CW & 31);
           // x (with a cap: the tanh's arguments) to probabilities, added up.
-          // GEN: with the mask and the bias' absolute value; EXACT: the cap for
-          // any argument.
+          // GEN: with the mask and the bias' absolute value; EXACT: arguments past
+          // FA_TANH_LIMIT too.
           auto add = [&](auto gen_c, auto exact_c) {
             constexpr bool GEN = decltype(gen_c)::value, EXACT = decltype(exact_c)::value;
             f2 dist = f2_pack(d0, d0 - 1.f);
@@ -382,9 +382,7 @@ kw_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
                   b = f2_fma(d, cslope, b);
                   dist = f2_add(dist, cstep);
                 }
-                if constexpr (CAP && EXACT) {
-                  z = f2_fma(f2_pack(tanh_mufu(x[e]), tanh_mufu(x[e + 1])), f2_pack(p.sc.cap_log2, p.sc.cap_log2), b);
-                } else if constexpr (CAP) {
+                if constexpr (CAP) {
                   const f2 u = f2_mul(v, v);
                   f2 q = f2_fma(u, ck5, ck4);
                   q = f2_fma(q, u, ck3);
@@ -392,6 +390,15 @@ kw_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUte
                   q = f2_fma(q, u, ck1);
                   q = f2_fma(q, u, ck0);
                   z = f2_fma(v, q, b);
+                  if constexpr (EXACT) {                                // each argument by itself: fa_score.cuh
+                    float u0, u1, z0, z1, e0, e1;
+                    f2_get(u, u0, u1);
+                    f2_get(z, z0, z1);
+                    f2_get(f2_fma(f2_pack(tanh_mufu(x[e]), tanh_mufu(x[e + 1])), f2_pack(p.sc.cap_log2, p.sc.cap_log2), b),
+                           e0, e1);
+                    constexpr float L2 = FA_TANH_LIMIT * FA_TANH_LIMIT;
+                    z = f2_pack(u0 <= L2 ? z0 : e0, u1 <= L2 ? z1 : e1);
+                  }
                 } else {
                   z = f2_fma(v, cscale, b);
                 }

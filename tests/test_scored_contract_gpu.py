@@ -109,3 +109,54 @@ def test_decode_shows_a_nan_query():
     assert torch.isnan(o[0, 1]).all() and torch.isnan(lse[0, 1]) and torch.isfinite(o[0, [0, 2, 3]]).all()
     assert torch.isnan(args["weights"][0, 0, :300]).all() and torch.isfinite(args["weights"][0, 1]).all()
     assert torch.isneginf(lse[1]).all() and not o[1].any() and torch.equal(args["weights"][1], w0[1])
+
+
+# ------------------------------------------------- what masked memory holds --
+
+NEIGHBOURS = {
+    "docs": dict(shape=(2, 4, 2, 330, 330, 64), docs=(60, 11)),
+    "docs_cap": dict(shape=(2, 4, 2, 330, 330, 128), docs=(60, 11), cap=6.0),
+    "docs_cap_bias": dict(shape=(2, 4, 1, 330, 330, 64), docs=(60, 11), cap=6.0, bias=True),
+    "docs_not_causal": dict(shape=(2, 2, 2, 200, 200, 64), docs=(60, 0), causal=False, bias=True),
+    "causal": dict(shape=(2, 4, 2, 260, 260, 128)),
+    "causal_cap": dict(shape=(2, 4, 2, 260, 300, 64), cap=6.0),
+    "prefix": dict(shape=(2, 2, 2, 260, 260, 64), prefix=[100, 31], bias=True),
+}
+
+
+@pytest.mark.parametrize("pad", (math.nan, math.inf, -3e38, 40.0))
+@pytest.mark.parametrize("c", (dict(B=3, Hq=4, Hkv=2, D=128, lens=[0, 37, 300], rows=320),
+                               dict(B=3, Hq=20, Hkv=1, D=64, lens=[1, 38, 299], rows=320),
+                               dict(B=2, Hq=24, Hkv=2, D=128, lens=[65, 301], rows=320, page=16),
+                               dict(B=2, Hq=8, Hkv=1, D=64, lens=[65, 301], rows=320, starts=[3, 290])), ids=range(4))
+def test_capped_decode_does_not_depend_on_rows_beside_its_own(c, pad):
+    """The same bits whatever stands in the row to append, behind it, and before the first row; called again, the row is there."""
+    q, k, v, args, _, _ = decode_problem(**c, append=True, cap=20.0, seed=31, pad=0.0)
+    w0 = args["weights"].clone()
+    want = [t.clone() for t in fa.decode_scored(q, k, v, **args)] + [args["weights"].clone()]
+    args["weights"].copy_(w0)
+    again = list(fa.decode_scored(q, k, v, **args)) + [args["weights"]]
+    assert all(torch.equal(a, b) for a, b in zip(again, want))
+    q, k, v, args, _, _ = decode_problem(**c, append=True, cap=20.0, seed=31, pad=pad)
+    for _ in range(2):
+        args["weights"].copy_(w0)
+        got = list(fa.decode_scored(q, k, v, **args)) + [args["weights"]]
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("value", (math.nan, math.inf, 3e38, 200.0))
+@pytest.mark.parametrize("name", ("docs", "docs_cap", "docs_cap_bias", "docs_not_causal"))
+def test_documents_do_not_change_bits_of_each_other(name, value):
+    """A document's keys, of any size, change no bit of o, lse and key weights of the others."""
+    c = dict(NEIGHBOURS[name])
+    p = S.Problem(*c.pop("shape"), seed=24, **c)
+    o, lse = forward(p)
+    w = fa.key_weights(*cuda(p, "q", "k"), lse, **p.how("cuda"))
+    hit = p.docs[1][0] == p.docs[1][0, 150]
+    p.k[0, hit] = value
+    o2, lse2 = forward(p)
+    w2 = fa.key_weights(*cuda(p, "q", "k"), lse2, **p.how("cuda"))
+    keep = ~hit.cuda()
+    assert torch.equal(o2[1], o[1]) and torch.equal(o2[0, keep], o[0, keep])
+    assert torch.equal(lse2[0][:, keep], lse[0][:, keep])
+    assert torch.equal(w2[1], w[1]) and torch.equal(w2[0][:, keep], w[0][:, keep])
