@@ -348,14 +348,14 @@ fa_status score_params(const fa_score* s, float scale, int causal, int Lq, int L
 
 // The tile facts of the documents, into `ws` (fa_scored_workspace_size bytes).
 fa_status launch_meta(fa::ScoreParams* sp, int B, int Lq, int Lk, void* ws, cudaStream_t st,
-                      uint32_t* zero8 = nullptr) {
+                      uint32_t* zero8 = nullptr, uint32_t* unseen = nullptr) {
   if (sp->q_docs == nullptr) return FA_OK;
   const int nq = (Lq + 127) / 128, nk = (Lk + 127) / 128;
   int4* q_meta = static_cast<int4*>(ws);
   int4* k_meta = q_meta + size_t(B) * nq;
   sp->counter = reinterpret_cast<int*>(k_meta + size_t(B) * nk);
   fa::score_meta_kernel<<<dim3(nq + nk, B), 256, 0, st>>>(sp->q_docs, sp->k_docs, Lq, Lk, q_meta, k_meta, sp->counter,
-                                                            zero8);
+                                                            zero8, unseen, sp->causal, sp->prefix);
   sp->q_meta = q_meta;
   sp->k_meta = k_meta;
   return launch_status();
@@ -509,10 +509,11 @@ fa_status run_bwd(const void* q, const void* k, const void* v, const void* o, co
   const unsigned amax_blocks = static_cast<unsigned>(std::min<size_t>((std::max(nq, nk) / 8 + 1023) / 1024, 148 * 4));
   const size_t chunks = size_t(B) * lq_pad * Hq * (D / 8);         // one thread per 16-byte chunk of a row
   const unsigned pre_blocks = static_cast<unsigned>(std::min<size_t>((chunks + 255) / 256, 148 * 16));
+  uint32_t* unseen = nullptr;                                      // keys that no query sees, with documents
   if (score == nullptr) {
     if (cudaMemsetAsync(dq_acc, 0, acc_bytes, st) != cudaSuccess || cudaMemsetAsync(amax, 0, 32, st) != cudaSuccess)
       return FA_ERR_CUDA;
-    fa::bwd_amax_kernel<<<dim3(amax_blocks, 4), 256, 0, st>>>(q_in, k_in, v_in, do_in, nq, nk, amax);
+    fa::bwd_amax_kernel<false><<<dim3(amax_blocks, 4), 256, 0, st>>>(q_in, k_in, v_in, do_in, nq, nk, amax);
     if (launch_status() != FA_OK) return FA_ERR_CUDA;
     fa::bwd_pre_kernel<false><<<pre_blocks, 256, 0, st>>>(static_cast<const uint16_t*>(o), nullptr, nullptr, do_in, q_in,
                                                           lse, amax, lse2, delta, q16, do16, B, Hq, Lq, lq_pad, D,
@@ -522,9 +523,11 @@ fa_status run_bwd(const void* q, const void* k, const void* v, const void* o, co
     // a chain of kernels that start while their predecessor ends; the first one
     // zeroes the maxima and the work counter, bwd_pre_kernel the dQ accumulator
     fa_status s;
+    if (sp.k_docs != nullptr) unseen = reinterpret_cast<uint32_t*>(reinterpret_cast<char*>(amax) + 256 + fa_scored_workspace_size(B, Lq, Lk));
     if (sp.k_docs == nullptr) {
       if (cudaMemsetAsync(amax, 0, 32, st) != cudaSuccess) return FA_ERR_CUDA;
-    } else if ((s = launch_meta(&sp, B, Lq, Lk, reinterpret_cast<char*>(amax) + 256, st, amax)) != FA_OK) {
+    } else if ((s = launch_meta(&sp, B, Lq, Lk, reinterpret_cast<char*>(amax) + 256, st, amax, unseen)) !=
+               FA_OK) {
       return s;
     }
     // without what rounding took off o, O is formed again, in two bf16 parts that
@@ -543,9 +546,11 @@ fa_status run_bwd(const void* q, const void* k, const void* v, const void* o, co
     if (sp.k_docs != nullptr || (causal && Lq > Lk)) {
       const size_t units = size_t(B) * ((std::max(Lq, Lk) + 31) / 32);
       s = launch_after(fa::bwd_amax_scored_kernel, dim3(static_cast<unsigned>(std::min<size_t>(units, 148 * 4)), 4),
-                       dim3(256), 0, st, q_in, k_in, v_in, do_in, amax, lse, sp.k_docs, B, Hq, Hkv, Lq, Lk, D);
+                       dim3(256), 0, st, q_in, k_in, v_in, do_in, amax, lse,
+                       static_cast<const uint32_t*>(unseen), B, Hq, Hkv, Lq, Lk, D);
     } else {
-      s = launch_after(fa::bwd_amax_kernel, dim3(amax_blocks, 4), dim3(256), 0, st, q_in, k_in, v_in, do_in, nq, nk, amax);
+      s = launch_after(fa::bwd_amax_kernel<true>, dim3(amax_blocks, 4), dim3(256), 0, st, q_in, k_in, v_in, do_in, nq, nk,
+                       amax);
     }
     if (s != FA_OK) return s;
     s = launch_after(fa::bwd_pre_kernel<true>, dim3(pre_blocks), dim3(256), 0, st, static_cast<const uint16_t*>(o), o_new,
@@ -570,6 +575,7 @@ fa_status run_bwd(const void* q, const void* k, const void* v, const void* o, co
   p.num_items = static_cast<int>(((Lk + 127) / 128) * B * Hkv);
   p.work_counter = counter;
   p.sc = sp;
+  p.unseen = unseen;
   if (sms <= 0) return FA_ERR_CUDA;
   const unsigned grid = static_cast<unsigned>(std::min(p.num_items, sms));
   fa_status s;
@@ -856,7 +862,8 @@ fa_status fa_fwd_scored(const void* q, const void* k, const void* v, void* o, vo
 
 size_t fa_bwd_scored_workspace_size(int B, int Hq, int Lq, int Lk, int D) {
   if (B <= 0 || Hq <= 0 || Lq < 0 || Lk < 0 || D <= 0) return 0;
-  return fa_bwd_workspace_size(B, Hq, Lq, D) + fa_scored_workspace_size(B, Lq, Lk);
+  return fa_bwd_workspace_size(B, Hq, Lq, D) + fa_scored_workspace_size(B, Lq, Lk) +
+         align_up(size_t(B) * ((size_t(Lk) + 127) / 128) * 16, 256);
 }
 
 fa_status fa_bwd_scored(const void* q, const void* k, const void* v, const void* o, const void* o_lo, const void* dO,

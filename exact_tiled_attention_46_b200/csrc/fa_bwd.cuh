@@ -61,7 +61,13 @@
 // plain kernel the two phases of a pair set the period; the cap lengthens the
 // first.  A key tile's query tiles run over the range
 // that shares a document with it.  Rows that see no key (LSE = -inf) and keys
-// without a document take part as zeros, whatever their memory holds.
+// that no query sees take part as zeros, whatever their memory holds, and count
+// for none of the input maxima.
+// An inf or NaN stays with the pairs that it belongs to, though 0 * NaN is NaN in
+// the products: inf and NaN are left out of the maxima and enter the products as
+// zeros; a query row that holds one (in q, dO, Delta or LSE) gets LSE = NaN
+// instead, and the thread of a key that does (in K or V) takes a NaN for a factor
+// of its scores, so that P and dS are NaN for its allowed pairs and 0 for the others.
 #pragma once
 #include "sm100.cuh"
 #include "fa_score.cuh"
@@ -100,7 +106,8 @@ struct BwdCfg {
   static constexpr int DQS_OFF = ROW_OFF + NQ * 1024;
   static constexpr int BAR_OFF = DQS_OFF + 4 * 8192;
   static constexpr int NBARS = 3 * KVB + 2 * NQ + 6 + 4 + 2 + 4 + 1;
-  static constexpr int SMEM_BYTES = BAR_OFF + NBARS * 8 + 32 + 1024;   // + TMEM address, item queue
+  static constexpr int BAD_OFF = BAR_OFF + NBARS * 8 + 32;   // after TMEM address and item queue
+  static constexpr int SMEM_BYTES = BAD_OFF + KVB * 512 + 1024;   // scored: per buffer and key, the last item that found an inf or NaN
   // TMEM columns
   static constexpr uint32_t T_S = 0, T_DP = 128, T_DV = 256, T_DK = 256 + D;
   static constexpr uint32_t T_DQ = DQ_IN_DP ? T_DP : 256 + 2 * D;   // buffer b at T_DQ + b * D
@@ -120,6 +127,7 @@ struct BwdParams {
   int g_fp32;
   uint64_t wait_limit_ns;
   ScoreParams sc;        // scored variants only
+  const uint32_t* unseen;  // scored with documents: 128 bits per key tile, the keys that no query sees
 };
 
 constexpr int BWD_LAUNCH_REGS = 128, BWD_WORK_REGS = 136, BWD_CTRL_REGS = 104;
@@ -137,7 +145,7 @@ enum : uint32_t {
 // accumulator, which then stay in L2 (all heads together do not).
 struct BwdItem {
   int b, hkv, j, i0, npairs;
-  int kuni, kneg, pre;   // scored: the one document of all keys or -1, some key has none, prefix length
+  int kuni, kmiss, pre;  // scored: the one document of all keys or -1, no query sees some key, prefix length
 };
 template <bool CAUSAL, int MOD = MOD_NONE>
 __device__ __forceinline__ BwdItem bwd_item(const BwdParams& p, int w) {
@@ -157,13 +165,13 @@ __device__ __forceinline__ BwdItem bwd_item(const BwdParams& p, int w) {
       I.i0 = first_q <= 0 ? 0 : (first_q >> 7);
     }
     I.kuni = -1;
-    I.kneg = 0;
+    I.kmiss = 0;
     if (sc.q_docs != nullptr) {
       const int4 m = sc.k_meta[static_cast<size_t>(I.b) * nk + I.j];
       I.kuni = m.x;
       I.i0 = max(I.i0, m.y);
       i1 = min(i1, m.z);
-      I.kneg = m.w;
+      I.kmiss = m.w;
     }
     I.npairs = max(0, i1 - I.i0) * (p.Hq / p.Hkv);
     return I;
@@ -205,7 +213,21 @@ __device__ __forceinline__ BwdScales bwd_scales(const uint32_t* amax, int D) {
 }
 
 // Largest |x| of q, k, v, dO (bf16) into amax[0..3] (float bits; zeroed
-// before).  blockIdx.y picks the tensor; one atomic per block.
+// before).  blockIdx.y picks the tensor; one atomic per block.  FINITE: of the
+// finite values; |x| + 0x80 carries an inf's or NaN's exponent past its 15 bits,
+// so that it ends below every finite one.
+template <bool FINITE>
+__device__ __forceinline__ uint32_t bwd_top(const uint4& w) {
+  const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+  uint32_t m = 0;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if constexpr (FINITE) m = __vmaxu2(m, ((ws[e] & 0x7fff7fffu) + 0x00800080u) & 0x7fff7fffu);
+    else m = max(m, max(ws[e] & 0x7fffu, (ws[e] >> 16) & 0x7fffu));
+  }
+  return FINITE ? max(m & 0xffffu, m >> 16) : m;
+}
+template <bool FINITE>
 __global__ void __launch_bounds__(256) bwd_amax_kernel(const uint16_t* q, const uint16_t* k, const uint16_t* v,
                                                        const uint16_t* dO, size_t nq, size_t nk, uint32_t* amax) {
   __shared__ uint32_t wmax[8];
@@ -222,11 +244,7 @@ __global__ void __launch_bounds__(256) bwd_amax_kernel(const uint16_t* q, const 
 #pragma unroll
     for (int u = 0; u < 4; ++u) w[u] = (i + u * stride < n8) ? p4[i + u * stride] : make_uint4(0, 0, 0, 0);
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const uint32_t ws[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) m = max(m, max(ws[e] & 0x7fffu, (ws[e] >> 16) & 0x7fffu));
-    }
+    for (int u = 0; u < 4; ++u) m = max(m, bwd_top<FINITE>(w[u]));
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
@@ -234,19 +252,20 @@ __global__ void __launch_bounds__(256) bwd_amax_kernel(const uint16_t* q, const 
   __syncthreads();
   if (threadIdx.x == 0) {
     for (int w = 1; w < static_cast<int>(blockDim.x >> 5); ++w) m = max(m, wmax[w]);
+    if (FINITE) m = m >= 0x80u ? m - 0x80u : 0u;
     if (m != 0) atomicMax(&amax[t], m << 16);      // |x| as float bits
   }
 }
 
 // The same where some rows do not count: rows of q and dO that see no key (lse =
-// -inf) and keys without a document, whose memory may hold anything.  A block
+// -inf) and keys that no query sees, whose memory may hold anything.  A block
 // takes 32 token rows at a time, finds out whether all of them count, and only
 // then looks chunks up one by one (looking up every chunk that would raise the
 // maximum cost 131 us against 63 us for the plain kernel at B8 H16 L4096 D64).
 __global__ void __launch_bounds__(256) bwd_amax_scored_kernel(const uint16_t* q, const uint16_t* k, const uint16_t* v,
                                                               const uint16_t* dO, uint32_t* amax, const float* lse,
-                                                              const int* k_docs, int B, int Hq, int Hkv, int Lq, int Lk,
-                                                              int D) {
+                                                              const uint32_t* unseen, int B, int Hq, int Hkv, int Lq,
+                                                              int Lk, int D) {
   __shared__ uint32_t wmax[8];
   pdl_next();
   pdl_wait();
@@ -256,21 +275,15 @@ __global__ void __launch_bounds__(256) bwd_amax_scored_kernel(const uint16_t* q,
   const int L = key_side ? Lk : Lq, H = key_side ? Hkv : Hq, cpr = D / 8, per_row = H * cpr;   // 16-byte chunks
   const int groups = (L + 31) / 32;
   uint32_t m = 0;
-  auto top = [](const uint4& w) {
-    const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-    uint32_t r = 0;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) r = max(r, max(ws[e] & 0x7fffu, (ws[e] >> 16) & 0x7fffu));
-    return r;
-  };
   for (int unit = blockIdx.x; unit < groups * B; unit += gridDim.x) {
     const int b = unit / groups, r0 = unit % groups * 32, rows = min(32, L - r0);
     const uint4* p4 = reinterpret_cast<const uint4*>(src) + (static_cast<size_t>(b) * L + r0) * per_row;
     const int n = rows * per_row;
     bool out = false;
+    uint32_t miss = 0;                             // these 32 keys' bits
     if (key_side) {
-      if (k_docs != nullptr && static_cast<int>(threadIdx.x) < rows)
-        out = k_docs[static_cast<size_t>(b) * Lk + r0 + threadIdx.x] < 0;
+      if (unseen != nullptr) miss = unseen[(static_cast<size_t>(b) * ((Lk + 127) / 128) + r0 / 128) * 4 + r0 / 32 % 4];
+      out = miss != 0;
     } else {
       for (int i = threadIdx.x; i < Hq * 32; i += 256)
         if ((i & 31) < rows) out |= lse[(static_cast<size_t>(b) * Hq + (i >> 5)) * Lq + r0 + (i & 31)] == -INFINITY;
@@ -281,14 +294,14 @@ __global__ void __launch_bounds__(256) bwd_amax_scored_kernel(const uint16_t* q,
 #pragma unroll
         for (int u = 0; u < 8; ++u) w[u] = c0 + u * 256 < n ? p4[c0 + u * 256] : make_uint4(0, 0, 0, 0);
 #pragma unroll
-        for (int u = 0; u < 8; ++u) m = max(m, top(w[u]));
+        for (int u = 0; u < 8; ++u) m = max(m, bwd_top<true>(w[u]));
       }
     } else {
       for (int c = threadIdx.x; c < n; c += 256) {
         const int r = r0 + c / per_row, h = c / cpr % H;
-        const bool counts = key_side ? k_docs[static_cast<size_t>(b) * Lk + r] >= 0
+        const bool counts = key_side ? !((miss >> (r - r0)) & 1u)
                                      : lse[(static_cast<size_t>(b) * Hq + h) * Lq + r] != -INFINITY;
-        if (counts) m = max(m, top(p4[c]));
+        if (counts) m = max(m, bwd_top<true>(p4[c]));
       }
     }
   }
@@ -298,6 +311,7 @@ __global__ void __launch_bounds__(256) bwd_amax_scored_kernel(const uint16_t* q,
   __syncthreads();
   if (threadIdx.x == 0) {
     for (int w = 1; w < 8; ++w) m = max(m, wmax[w]);
+    m = m >= 0x80u ? m - 0x80u : 0u;
     if (m != 0) atomicMax(&amax[t], m << 16);      // |x| as float bits
   }
 }
@@ -310,7 +324,8 @@ __global__ void __launch_bounds__(256) bwd_amax_scored_kernel(const uint16_t* q,
 // (lse = -inf) become zeros; o_lo is what o's rounding took off.  With o_new,
 // o_new + o_lo is O formed again, and o_lo holds for an element of o that is its
 // rounding: one further off (the o of a call over more keys than this one's) is
-// taken as it is.  q16 may be o_new, and do16 o_lo.
+// taken as it is.  q16 may be o_new, and do16 o_lo.  A row with an inf or NaN in
+// q, dO, O or LSE: zeros, with LSE = NaN and Delta = 0.
 template <bool SCORED>
 __global__ void __launch_bounds__(256) bwd_pre_kernel(const uint16_t* o, const uint16_t* o_new, const uint16_t* o_lo,
                                                       const uint16_t* dO,
@@ -332,8 +347,9 @@ __global__ void __launch_bounds__(256) bwd_pre_kernel(const uint16_t* o, const u
     const int i = static_cast<int>(bi % Lq_pad);
     const int b = static_cast<int>(bi / Lq_pad);
     float acc = 0.f;
+    uint32_t hq[4], hd[4];
+    const size_t off = ((size_t(b) * Lq + i) * Hq + h) * D / 8 + c;       // in 16-byte chunks
     if (i < Lq) {
-      const size_t off = ((size_t(b) * Lq + i) * Hq + h) * D / 8 + c;     // in 16-byte chunks
       uint4 a = reinterpret_cast<const uint4*>(o)[off];
       uint4 g = reinterpret_cast<const uint4*>(dO)[off];
       uint4 x = reinterpret_cast<const uint4*>(q)[off];
@@ -349,7 +365,6 @@ __global__ void __launch_bounds__(256) bwd_pre_kernel(const uint16_t* o, const u
         return fabsf(x - a) <= 0x1.01p-8f * fabsf(x) ? x : a;
       };
       const uint32_t av[4] = {a.x, a.y, a.z, a.w}, gv[4] = {g.x, g.y, g.z, g.w}, xv[4] = {x.x, x.y, x.z, x.w};
-      uint32_t hq[4], hd[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const float g0 = __uint_as_float(gv[e] << 16), g1 = __uint_as_float(gv[e] & 0xffff0000u);
@@ -363,17 +378,21 @@ __global__ void __launch_bounds__(256) bwd_pre_kernel(const uint16_t* o, const u
         hd[e] = pack_f16x2(g0 * fdo, g1 * fdo);
         hq[e] = pack_f16x2(__uint_as_float(xv[e] << 16) * fq, __uint_as_float(xv[e] & 0xffff0000u) * fq);
       }
+      if (SCORED && !(finite8(x) && finite8(g))) acc = __int_as_float(0x7fffffff);
       if (SCORED) {                                // the dQ accumulator, zeroed here instead of by a launch of its own
         const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
         reinterpret_cast<float4*>(zero_acc)[2 * off] = z;
         reinterpret_cast<float4*>(zero_acc)[2 * off + 1] = z;
       }
-      reinterpret_cast<uint4*>(q16)[off] = make_uint4(hq[0], hq[1], hq[2], hq[3]);
-      reinterpret_cast<uint4*>(do16)[off] = make_uint4(hd[0], hd[1], hd[2], hd[3]);
     }
     // the row's chunks are cpr consecutive lanes of one warp (every lane of the
     // warp takes part: the loop bound is a multiple of 32)
     for (int m = 1; m < cpr; m <<= 1) acc += __shfl_xor_sync(0xffffffffu, acc, m);
+    const bool bad = SCORED && !(fabsf(acc) < INFINITY);
+    if (i < Lq) {
+      reinterpret_cast<uint4*>(q16)[off] = bad ? make_uint4(0u, 0u, 0u, 0u) : make_uint4(hq[0], hq[1], hq[2], hq[3]);
+      reinterpret_cast<uint4*>(do16)[off] = bad ? make_uint4(0u, 0u, 0u, 0u) : make_uint4(hd[0], hd[1], hd[2], hd[3]);
+    }
     if (c == 0) {
       const size_t dst = (size_t(b) * Hq + h) * Lq_pad + i;
       if (i >= Lq) {
@@ -381,8 +400,8 @@ __global__ void __launch_bounds__(256) bwd_pre_kernel(const uint16_t* o, const u
         delta[dst] = 0.f;
       } else {
         const float l = lse[(size_t(b) * Hq + h) * Lq + i];
-        lse2[dst] = (l == -INFINITY) ? INFINITY : l * 1.4426950408889634f;
-        delta[dst] = acc * fdelta;
+        lse2[dst] = bad ? __int_as_float(0x7fffffff) : (l == -INFINITY) ? INFINITY : l * 1.4426950408889634f;
+        delta[dst] = bad ? 0.f : acc * fdelta;
       }
     }
   }
@@ -440,7 +459,7 @@ __device__ __forceinline__ void bwd_score(float (&x)[16], float (&dt)[16], const
 // whatever the score, so only for caps up to BWD_MUFU_CAP (2^-14, an eighth of
 // P's own fp16 rounding); larger ones run the variant with a bias, at slope 0.
 constexpr float BWD_MUFU_CAP = 256.f;
-__device__ __forceinline__ void bwd_capped(float (&x)[16], float* pv, const float* lse2, const ScoreParams& sc, float ysc,
+__device__ __forceinline__ void bwd_capped(float (&x)[16], float* pv, const float* lse2, float cap_log2, float ysc,
                                            uint32_t bits, bool masked) {
   f2 dt[8];
   const f2 one = f2_dup(1.f);
@@ -451,7 +470,7 @@ __device__ __forceinline__ void bwd_capped(float (&x)[16], float* pv, const floa
     x[2 * c + 1] = t1;
     dt[c] = f2_fma(f2_pack(-t0, -t1), f2_pack(t0, t1), one);
   }
-  const f2 cap2 = f2_pack(sc.cap_log2, sc.cap_log2);
+  const f2 cap2 = f2_pack(cap_log2, cap_log2);
 #pragma unroll
   for (int c4 = 0; c4 < 4; ++c4) {
     const float4 l4 = *reinterpret_cast<const float4*>(lse2 + 4 * c4);
@@ -503,6 +522,7 @@ bwd_main_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
   uint64_t* mma_done = item_empty + 2;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + C::NBARS);
   volatile int* item_w = reinterpret_cast<volatile int*>(tmem_holder + 4);   // [2] item numbers (-1: none left)
+  [[maybe_unused]] volatile int* k_bad = reinterpret_cast<volatile int*>(smem + C::BAD_OFF);   // [KVB][128]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint64_t lim = p.wait_limit_ns;
@@ -527,6 +547,7 @@ bwd_main_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     fence_mbar_init();
   }
   if (warp == 14) { tmem_alloc(tmem_holder, 512); tmem_relinquish(); }
+  if (MOD != MOD_NONE && static_cast<int>(threadIdx.x) < C::KVB * 128) k_bad[threadIdx.x] = 0;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -736,10 +757,14 @@ bwd_main_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
           const float f = (c < C::TILE / 16) ? fk : fv;
           uint4 w = kv4[c];
           if constexpr (MOD != MOD_NONE) {
-            if (I.kneg) {                          // keys without a document: zeros
-              const int kr = I.j * 128 + ((c * 16) & 16383) / 128;
-              if (kr < p.Lk && p.sc.k_docs[static_cast<size_t>(I.b) * p.Lk + kr] < 0) w = make_uint4(0u, 0u, 0u, 0u);
+            const int kr = ((c * 16) & 16383) / 128;   // row of the tile
+            bool drop = false;
+            if (I.kmiss) drop = (p.unseen[(static_cast<size_t>(I.b) * ((p.Lk + 127) >> 7) + I.j) * 4 + (kr >> 5)] >> (kr & 31)) & 1u;
+            if (!drop && !finite8(w)) {
+              k_bad[u * 128 + kr] = it + 1;
+              drop = true;
             }
+            if (drop) w = make_uint4(0u, 0u, 0u, 0u);
           }
           const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
           uint32_t hs[4];
@@ -750,6 +775,13 @@ bwd_main_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         }
         fence_proxy_async_smem();
         mbar_arrive(&kv_conv[u]);
+      }
+      [[maybe_unused]] bool bad = false;             // scored: this key holds an inf or NaN
+      [[maybe_unused]] float mul = 1.f;              // scored: factor of the score's last step, NaN for such a key
+      if constexpr (MOD != MOD_NONE) {
+        npairs_ok = npairs_ok && mbar_wait_warp(&kv_conv[u], (it / C::KVB) & 1, lim, W_BWD_KV);
+        bad = k_bad[u * 128 + r] == it + 1;
+        mul = bad ? __int_as_float(0x7fffffff) : (MOD & MOD_CAP) ? p.sc.cap_log2 : sl2;
       }
       for (int n = 0; npairs_ok && n < I.npairs; ++n) {
         const int g = gp + n, s = g % NQ;
@@ -780,7 +812,8 @@ bwd_main_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             doc_bits(kid, qid, m);
           }
           if constexpr ((MOD & MOD_BIAS) != 0)
-            slope2 = p.sc.slopes != nullptr ? p.sc.slopes[I.hkv * G + n % G] * LOG2E : 0.f;
+            slope2 = bad ? __int_as_float(0x7fffffff)
+                         : p.sc.slopes != nullptr ? p.sc.slopes[I.hkv * G + n % G] * LOG2E : 0.f;
         }
         if (!(npairs_ok = mbar_wait_warp(s_full, g & 1, lim, W_BWD_SDP))) break;
         tc_fence_after();
@@ -802,7 +835,7 @@ bwd_main_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
           uint32_t ph[8];
           if constexpr (D == 64 && (MOD & (MOD_CAP | MOD_BIAS)) == MOD_CAP) {
             float (&x)[16] = *reinterpret_cast<float(*)[16]>(sv);
-            bwd_capped(x, &pv[sc * 16], lse2 + c0, p.sc, ysc, m[sc >> 1] >> ((sc & 1) * 16), part);
+            bwd_capped(x, &pv[sc * 16], lse2 + c0, mul, ysc, m[sc >> 1] >> ((sc & 1) * 16), part);
 #pragma unroll
             for (int t = 0; t < 8; ++t) ph[t] = pack_f16x2(x[2 * t], x[2 * t + 1]);
           } else if constexpr (MOD != MOD_NONE) {
@@ -810,7 +843,7 @@ bwd_main_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             float dt[16];                                // 1 - t^2 of the cap
             if constexpr ((MOD & (MOD_CAP | MOD_BIAS)) != 0)
               bwd_score<MOD>(x, dt, p.sc, sl2, ysc, slope2, static_cast<float>(key - off - i * 128 - c0));
-            const float mul = (MOD & MOD_BIAS) ? 1.f : (MOD & MOD_CAP) ? p.sc.cap_log2 : sl2;
+            const float mul1 = (MOD & MOD_BIAS) ? 1.f : mul;   // with a bias its slope carries the NaN
             const uint32_t bits = m[sc >> 1] >> ((sc & 1) * 16);
 #pragma unroll
             for (int t4 = 0; t4 < 4; ++t4) {
@@ -819,7 +852,7 @@ bwd_main_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
               for (int u = 0; u < 2; ++u) {
                 const int t = 2 * t4 + u;
                 float x0, x1;
-                ffma2(x0, x1, x[2 * t], x[2 * t + 1], mul, mul, -(u ? l4.z : l4.x), -(u ? l4.w : l4.y));
+                ffma2(x0, x1, x[2 * t], x[2 * t + 1], mul1, mul1, -(u ? l4.z : l4.x), -(u ? l4.w : l4.y));
                 float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
                 if (part) {
                   p0 = (bits >> (2 * t)) & 1u ? p0 : 0.f;

@@ -19,8 +19,8 @@ struct ScoreParams {
   const int* k_docs;       // [B, Lk] or nullptr
   const int* prefix;       // [B] or nullptr
   // per 128-row tile {the one document of all its rows or -1, first tile of the
-  // other side that shares a document with it, one past the last, some row has
-  // no document}; only with documents
+  // other side that shares a document with it, one past the last, some key is
+  // seen by no query (where that was asked for)}; only with documents
   const int4* q_meta;      // [B, ceil(Lq / 128)]
   const int4* k_meta;      // [B, ceil(Lk / 128)]
   int causal;
@@ -43,9 +43,13 @@ __device__ __forceinline__ int score_prefix(const ScoreParams& s, int b, int Lk)
 // row; for ids in any order the range may hold tiles without a common document,
 // and the element masks decide).  Reads 4 (Lq + Lk) bytes per block out of L2:
 // 3 us at L = 1000, 7 at B8 L4096 (of a forward of 425), hidden in part by the
-// next kernel's start.
+// next kernel's start.  `unseen` (or nullptr) receives 128 bits per key tile: the
+// keys that no query may see.  A warp looks its 32 keys up among the range's
+// queries, 32 at a time from the first that position allows, until all are found
+// (packed documents: within the first steps).
 __global__ void __launch_bounds__(256) score_meta_kernel(const int* q_docs, const int* k_docs, int Lq, int Lk,
-                                                         int4* q_meta, int4* k_meta, int* counter, uint32_t* zero8) {
+                                                         int4* q_meta, int4* k_meta, int* counter, uint32_t* zero8,
+                                                         uint32_t* unseen, int causal, const int* prefix) {
   pdl_next();
   const int nq = (Lq + 127) >> 7, nk = (Lk + 127) >> 7;
   const int b = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -84,16 +88,40 @@ __global__ void __launch_bounds__(256) score_meta_kernel(const int* q_docs, cons
     }
   if (lane == 0) { s_lo[warp] = lo; s_hi[warp] = hi; }
   __syncthreads();
+  for (int w = 0; w < 8; ++w) { lo = min(lo, s_lo[w]); hi = max(hi, s_hi[w]); }
+  if (lo > hi) lo = hi = 0;
+  bool miss = false;                             // this thread's key is seen by no query
+  if (unseen != nullptr && !q_side) {
+    if (warp < 4) {
+      const int key = tile * 128 + warp * 32 + lane, kid = key < Lk ? mine[key] : -1;
+      const int pre = prefix != nullptr ? prefix[b] : 0;
+      const int from = causal && key >= pre ? max(0, key - (Lk - Lq)) : 0;   // first query that position allows
+      const bool live = kid >= 0;
+      bool seen = key >= Lk;
+      const int q1 = min(hi * 128, Lq);
+      for (int q0 = max(lo * 128, __reduce_min_sync(0xffffffffu, live ? from : INT_MAX) & ~31); q0 < q1; q0 += 32) {
+        if (__all_sync(0xffffffffu, seen || !live)) break;
+        const int qd = q0 + lane < q1 ? other[q0 + lane] : -1;
+#pragma unroll
+        for (int u = 0; u < 32; ++u) {
+          const int d = __shfl_sync(0xffffffffu, qd, u);
+          seen |= live && d == kid && q0 + u >= from;
+        }
+      }
+      miss = !seen;
+      const uint32_t bits = __ballot_sync(0xffffffffu, miss);
+      if (lane == 0) unseen[(static_cast<size_t>(b) * nk + tile) * 4 + warp] = bits;
+    }
+    miss = __syncthreads_or(miss);
+  }
   if (threadIdx.x == 0) {
     if (blockIdx.x == 0 && b == 0) {
       *counter = 0;
       if (zero8 != nullptr)                      // eight words that the caller's next kernel adds to
         for (int i = 0; i < 8; ++i) zero8[i] = 0;
     }
-    for (int w = 1; w < 8; ++w) { lo = min(lo, s_lo[w]); hi = max(hi, s_hi[w]); }
-    if (lo > hi) lo = hi = 0;
     (q_side ? q_meta + static_cast<size_t>(b) * nq : k_meta + static_cast<size_t>(b) * nk)[tile] =
-        make_int4(mn == mx && !neg ? mn : -1, lo, hi, neg ? 1 : 0);
+        make_int4(mn == mx && !neg ? mn : -1, lo, hi, miss ? 1 : 0);
   }
 }
 
@@ -124,6 +152,16 @@ __device__ __forceinline__ void doc_bits(int id, const int (&other)[W], uint32_t
   }
 #pragma unroll
   for (int w = 0; w < W; ++w) m[w] &= d[w];
+}
+
+// No inf or NaN among eight bf16: x * 0 + a keeps a NaN once any x is not finite.
+__device__ __forceinline__ bool finite8(const uint4& w) {
+  const __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
+  __nv_bfloat162 a = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&w.x), zero);
+  a = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&w.y), zero, a);
+  a = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&w.z), zero, a);
+  a = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&w.w), zero, a);
+  return !__hisnan(a.x) && !__hisnan(a.y);
 }
 
 // -------------------------------------------------------------------- cap --

@@ -274,8 +274,9 @@ fa_status fa_attn_merge(const float* o_a, const float* lse_a, const float* o_b, 
  * device (prefix is clamped to [0, Lk]).  A query that sees no key gets O = 0,
  * LSE = -inf and zero gradients, and what a pair that is not allowed holds (an
  * inf or NaN in a masked key or value, or anywhere in a token without a
- * document) reaches no other row; a query that sees a v row with an inf or NaN
- * in a tile that it sees only in part gets NaN in all of its D entries.
+ * document) reaches no other row, in any of the calls below; a query that sees a
+ * v row with an inf or NaN gets NaN in all of its D entries where some query of
+ * its 256 does not see all of that row's 128-key tile.
  * Documents may stand in any order; packed ones (numbers that only grow along
  * the row) let the kernels skip the key tiles of other documents.  The slopes
  * are constants: no gradient is formed for them.  With slopes, Lq and Lk must
@@ -315,8 +316,12 @@ fa_status fa_fwd_scored(const void* q, const void* k, const void* v, void* o, vo
  * and lse.  Without o_lo (NULL) the call forms O to 16 bits again (a forward's
  * time more) and corrects every element of o that is its rounding; an o of other
  * keys (a part of a context, under its whole log-sums) is taken as it is.
- * The tanh's derivative is part of dq and dk.  An inf or NaN in an allowed pair
- * gives non-finite gradients.  workspace: at least
+ * The tanh's derivative is part of dq and dk.  A query with an inf or NaN in q,
+ * dO, o or its lse, and a key with one in k or v, get NaN gradients, and so do the
+ * keys that such a query sees and the queries that see such a key; no others do.
+ * The products run on fp16 operands as in fa_bwd: each tensor's largest finite
+ * magnitude, of the rows that see or are seen by some other, sets its scale, and
+ * values below 2^-22 of it lose bits.  workspace: at least
  * fa_bwd_scored_workspace_size() bytes, 256-byte aligned.
  */
 size_t fa_bwd_scored_workspace_size(int B, int Hq, int Lq, int Lk, int D);

@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import exact_tiled_attention_46_b200 as fa
+import oracle.scored as osc
 
 import scored as S
 from parity import need_gpu
@@ -112,7 +113,6 @@ def test_decode_shows_a_nan_query():
 
 
 # ------------------------------------------------- what masked memory holds --
-
 NEIGHBOURS = {
     "docs": dict(shape=(2, 4, 2, 330, 330, 64), docs=(60, 11)),
     "docs_cap": dict(shape=(2, 4, 2, 330, 330, 128), docs=(60, 11), cap=6.0),
@@ -122,6 +122,17 @@ NEIGHBOURS = {
     "causal_cap": dict(shape=(2, 4, 2, 260, 300, 64), cap=6.0),
     "prefix": dict(shape=(2, 2, 2, 260, 260, 64), prefix=[100, 31], bias=True),
 }
+
+
+def gradients(p, **kw):
+    lo = torch.empty_like(p.q).cuda()
+    o, lse = forward(p, o_lo=lo)
+    return o, lse, fa.bwd_scored(*cuda(p, "q", "k", "v"), o, p.do.cuda(), lse, grad_dtype=torch.float32, **p.how("cuda"), **kw)
+
+
+def same_sums(a, b, mag):
+    """dQ sums its key tiles in any order: a rounding step of fp32 per addition, of sums of at most `mag`."""
+    return float((a - b).abs().max() if a.numel() else 0.0) <= 2.0 ** -19 * mag
 
 
 @pytest.mark.parametrize("pad", (math.nan, math.inf, -3e38, 40.0))
@@ -160,3 +171,84 @@ def test_documents_do_not_change_bits_of_each_other(name, value):
     assert torch.equal(o2[1], o[1]) and torch.equal(o2[0, keep], o[0, keep])
     assert torch.equal(lse2[0][:, keep], lse[0][:, keep])
     assert torch.equal(w2[1], w[1]) and torch.equal(w2[0][:, keep], w[0][:, keep])
+
+@pytest.mark.parametrize("which", ("q", "k", "v", "do"))
+@pytest.mark.parametrize("value", (math.nan, -math.inf))
+@pytest.mark.parametrize("name", NEIGHBOURS)
+def test_gradient_of_an_inf_or_nan_stays_with_its_pairs(name, value, which):
+    """One element of one row of batch 0: NaN gradients for that row and for what is paired with it, nothing elsewhere."""
+    c = dict(NEIGHBOURS[name])
+    p = S.Problem(*c.pop("shape"), seed=21, **c)
+    B, Hq, Hkv, Lq, Lk, D = p.shape
+    _, _, ref = gradients(p)
+    x, at = getattr(p, which), 150
+    head = (x.shape[2] - 1)
+    top = x.abs().max()
+    x[0, at, head, 9] = 0.0
+    assert x.abs().max() == top                                  # the scale of the others stays
+    x[0, at, head, 9] = value
+    o, lse, got = gradients(p)
+    G = Hq // Hkv
+    heads = list(range(head * G, head * G + G)) if which in "kv" else [head]
+    ok = osc.scored_mask(0, Lq, Lk, p.causal, *(p.oracle_how()[n] for n in ("q_docs", "k_docs", "prefix")))
+    nan_q, nan_k = np.zeros((B, Hq, Lq), bool), np.zeros((B, Hkv, Lk), bool)
+    for h in heads:
+        rows = ~np.isfinite(f64(o)[0, :, h]).all(axis=1) | np.isnan(f64(lse)[0, h])
+        if which in ("q", "do"):
+            rows[at] |= ok[at].any()
+        nan_k[0, h // G] |= ok[rows].any(axis=0)
+        nan_q[0, h] = rows
+        if which in "kv":
+            nan_q[0, h] |= ok[:, at]
+            nan_k[0, h // G, at] |= ok[:, at].any()
+    assert nan_q.any() and nan_k.any() and not nan_q[0, heads[0]].all()
+    # keys whose queries all give what they gave (an infinite key may leave its queries a finite, other softmax)
+    other = nan_k.copy()
+    if which in "kv":
+        other[0, head] |= ok[ok[:, at]].any(axis=0)
+    for g, r, bad, new in zip(got, ref, (nan_q, nan_k, nan_k), (nan_q, other, other)):
+        bad, new = (torch.from_numpy(m).permute(0, 2, 1).cuda() for m in (bad, new))
+        assert torch.isnan(g[bad]).all() and torch.isfinite(g[~bad]).all()
+        assert same_sums(g[~new], r[~new], 64.0) if g is got[0] else torch.equal(g[~new], r[~new])
+
+
+@pytest.mark.parametrize("D,cap,bias", [(64, 0.0, False), (128, 7.0, False), (64, 7.0, False), (64, 0.0, True), (128, 7.0, True)])
+@pytest.mark.parametrize("causal", (True, False))
+def test_keys_that_no_query_sees_leave_the_gradient_alone(D, cap, bias, causal):
+    """Documents before the window's own, in its tiles and in tiles of their own: NaN, inf and huge numbers there."""
+    Lq, Lk = 200, 700
+    kd = np.repeat(np.arange(7), 100)[None, :].astype(np.int32) + np.array([[0], [3]], np.int32)
+    p = S.Problem(2, 4, 2, Lq, Lk, D, causal=causal, cap=cap, bias=bias, docs=kd, seed=22)
+    p.docs[0][0, :], p.docs[0][1, :] = torch.tensor([5, 6]).repeat_interleave(100), 9      # of batch 1 only the last document
+    hidden = ~np.isin(np.arange(Lk)[None, :] // 100, (5, 6)) | (np.array([[0], [1]]) & (np.arange(Lk)[None, :] // 100 == 5))
+    hidden = torch.from_numpy(hidden.astype(bool))
+    o, lse, ref = gradients(p)
+    S.check_bwd(p, *ref, bf16_output=False, fine=True)
+    for bad_k, bad_v in ((math.nan, math.inf), (3e38, -3e38), (-math.inf, 1e30)):
+        p.k[hidden], p.v[hidden] = bad_k, bad_v
+        o2, lse2, got = gradients(p)
+        assert torch.equal(o2, o) and torch.equal(lse2, lse)
+        assert torch.equal(got[1], ref[1]) and torch.equal(got[2], ref[2])
+        assert not got[1][hidden.cuda()].any() and not got[2][hidden.cuda()].any()
+        assert torch.isfinite(got[0]).all() and same_sums(got[0], ref[0], 64.0)
+
+
+def test_keys_of_documents_in_any_order_that_no_query_has():
+    """Document numbers in no order on both sides; a seen key after the causal edge counts as unseen."""
+    rng = np.random.default_rng(23)
+    kd = rng.integers(0, 40, (2, 500)).astype(np.int32)
+    p = S.Problem(2, 2, 2, 300, 500, 64, docs=kd, seed=23)
+    qd = rng.integers(20, 60, (2, 300)).astype(np.int32)
+    p.docs = (torch.from_numpy(qd), p.docs[1])
+    for causal, prefix in ((True, None), (False, None), (True, [130, 0])):
+        p.causal, p.prefix = causal, None if prefix is None else torch.tensor(prefix, dtype=torch.int32)
+        ok = np.stack([osc.scored_mask(b, 300, 500, causal, qd, kd, prefix) for b in range(2)])
+        hidden = torch.from_numpy(~ok.any(axis=1))
+        k, v = p.k.clone(), p.v.clone()
+        _, _, ref = gradients(p)
+        S.check_bwd(p, *ref, bf16_output=False, fine=True)
+        p.k[hidden], p.v[hidden] = 2e38, math.nan
+        _, _, got = gradients(p)
+        assert torch.equal(got[1], ref[1]) and torch.equal(got[2], ref[2]) and same_sums(got[0], ref[0], 64.0)
+        p.k, p.v = k, v
+
