@@ -378,7 +378,7 @@ __global__ void __launch_bounds__(256) bwd_pre_kernel(const uint16_t* o, const u
         hd[e] = pack_f16x2(g0 * fdo, g1 * fdo);
         hq[e] = pack_f16x2(__uint_as_float(xv[e] << 16) * fq, __uint_as_float(xv[e] & 0xffff0000u) * fq);
       }
-      if (SCORED && !(finite8(x) && finite8(g))) acc = __int_as_float(0x7fffffff);
+      if (SCORED && is_nan2(poison8(x, poison8(g, __float2bfloat162_rn(0.f))))) acc = __int_as_float(0x7fffffff);
       if (SCORED) {                                // the dQ accumulator, zeroed here instead of by a launch of its own
         const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
         reinterpret_cast<float4*>(zero_acc)[2 * off] = z;
@@ -427,18 +427,17 @@ __global__ void __launch_bounds__(256) bwd_post_kernel(const float* acc, void* d
 
 // Scored variants: raw products of one key and 16 consecutive queries towards
 // scores in log2 units, with 1 - t^2 of the cap beside them (without a bias a
-// factor is still to come: cap_log2 after the cap, else sl2).  d0 is the distance
+// factor is still to come).  mul: cap_log2 with a cap, else sl2.  d0 is the distance
 // key - query position of column 0; distances are whole numbers below 2^24, exact.
 template <int MOD>
-__device__ __forceinline__ void bwd_score(float (&x)[16], float (&dt)[16], const ScoreParams& sc, float sl2, float ysc,
-                                          float slope2, float d0) {
+__device__ __forceinline__ void bwd_score(float (&x)[16], float (&dt)[16], float mul, float ysc, float slope2,
+                                          float d0) {
   if constexpr ((MOD & MOD_CAP) != 0) {
     cap_tile(x, ysc);                                // x = t
 #pragma unroll
     for (int c = 0; c < 16; c += 2) ffma2(dt[c], dt[c + 1], x[c], x[c + 1], -x[c], -x[c + 1], 1.f, 1.f);
   }
   if constexpr ((MOD & MOD_BIAS) != 0) {
-    const float mul = (MOD & MOD_CAP) ? sc.cap_log2 : sl2;
     float t0 = d0, t1 = d0 - 1.f;
 #pragma unroll
     for (int c = 0; c < 16; c += 2) {
@@ -547,7 +546,8 @@ bwd_main_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     fence_mbar_init();
   }
   if (warp == 14) { tmem_alloc(tmem_holder, 512); tmem_relinquish(); }
-  if (MOD != MOD_NONE && static_cast<int>(threadIdx.x) < C::KVB * 128) k_bad[threadIdx.x] = 0;
+  if (MOD != MOD_NONE && warp == 15)
+    for (int i = lane; i < C::KVB * 128; i += 32) k_bad[i] = 0;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -752,20 +752,12 @@ bwd_main_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         const float fk = bwd_pow2(sc_in.kk), fv = bwd_pow2(sc_in.kv);
         uint4* kv4 = reinterpret_cast<uint4*>(smem + u * 2 * C::TILE + C::K_OFF);   // K then V, contiguous
         constexpr int N16 = 2 * C::TILE / 16;
+        [[maybe_unused]] __nv_bfloat162 acc = __float2bfloat162_rn(0.f);
 #pragma unroll 4
         for (int c = threadIdx.x; c < N16; c += 256) {
           const float f = (c < C::TILE / 16) ? fk : fv;
-          uint4 w = kv4[c];
-          if constexpr (MOD != MOD_NONE) {
-            const int kr = ((c * 16) & 16383) / 128;   // row of the tile
-            bool drop = false;
-            if (I.kmiss) drop = (p.unseen[(static_cast<size_t>(I.b) * ((p.Lk + 127) >> 7) + I.j) * 4 + (kr >> 5)] >> (kr & 31)) & 1u;
-            if (!drop && !finite8(w)) {
-              k_bad[u * 128 + kr] = it + 1;
-              drop = true;
-            }
-            if (drop) w = make_uint4(0u, 0u, 0u, 0u);
-          }
+          const uint4 w = kv4[c];
+          if constexpr (MOD != MOD_NONE) acc = poison8(w, acc);
           const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
           uint32_t hs[4];
 #pragma unroll
@@ -773,16 +765,26 @@ bwd_main_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             hs[e] = pack_f16x2(__uint_as_float(ws[e] << 16) * f, __uint_as_float(ws[e] & 0xffff0000u) * f);
           kv4[c] = make_uint4(hs[0], hs[1], hs[2], hs[3]);
         }
+        if constexpr (MOD != MOD_NONE) {
+          // seldom: zeros for the keys that no query sees and for what is not
+          // finite (the scales keep every finite value finite in fp16)
+          if (I.kmiss || is_nan2(acc)) {
+            const uint32_t* miss = p.unseen + (static_cast<size_t>(I.b) * ((p.Lk + 127) >> 7) + I.j) * 4;
+            for (int c = threadIdx.x; c < N16; c += 256) {
+              const int kr = ((c * 16) & 16383) / 128;   // row of the tile
+              const bool drop = I.kmiss && ((miss[kr >> 5] >> (kr & 31)) & 1u);
+              const uint4 w = kv4[c];
+              bool bad = false;
+              for (const uint32_t x : {w.x, w.y, w.z, w.w}) bad |= (x & 0x7c00u) == 0x7c00u || (x & 0x7c000000u) == 0x7c000000u;
+              if (!drop && bad) k_bad[u * 128 + kr] = it + 1;
+              if (drop || bad) kv4[c] = make_uint4(0u, 0u, 0u, 0u);
+            }
+          }
+        }
         fence_proxy_async_smem();
         mbar_arrive(&kv_conv[u]);
       }
-      [[maybe_unused]] bool bad = false;             // scored: this key holds an inf or NaN
-      [[maybe_unused]] float mul = 1.f;              // scored: factor of the score's last step, NaN for such a key
-      if constexpr (MOD != MOD_NONE) {
-        npairs_ok = npairs_ok && mbar_wait_warp(&kv_conv[u], (it / C::KVB) & 1, lim, W_BWD_KV);
-        bad = k_bad[u * 128 + r] == it + 1;
-        mul = bad ? __int_as_float(0x7fffffff) : (MOD & MOD_CAP) ? p.sc.cap_log2 : sl2;
-      }
+      [[maybe_unused]] float mul = 1.f;              // scored: factor of the scores, NaN for a key with an inf or NaN
       for (int n = 0; npairs_ok && n < I.npairs; ++n) {
         const int g = gp + n, s = g % NQ;
         const int i = I.i0 + n / G;
@@ -812,8 +814,11 @@ bwd_main_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             doc_bits(kid, qid, m);
           }
           if constexpr ((MOD & MOD_BIAS) != 0)
-            slope2 = bad ? __int_as_float(0x7fffffff)
-                         : p.sc.slopes != nullptr ? p.sc.slopes[I.hkv * G + n % G] * LOG2E : 0.f;
+            slope2 = p.sc.slopes != nullptr ? p.sc.slopes[I.hkv * G + n % G] * LOG2E : 0.f;
+          if (n == 0) {                              // after the masks: their loads run beside the other warps' conversion
+            if (!(npairs_ok = mbar_wait_warp(&kv_conv[u], (it / C::KVB) & 1, lim, W_BWD_KV))) break;
+            mul = k_bad[u * 128 + r] == it + 1 ? __int_as_float(0x7fffffff) : (MOD & MOD_CAP) ? p.sc.cap_log2 : sl2;
+          }
         }
         if (!(npairs_ok = mbar_wait_warp(s_full, g & 1, lim, W_BWD_SDP))) break;
         tc_fence_after();
@@ -842,8 +847,8 @@ bwd_main_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             float (&x)[16] = *reinterpret_cast<float(*)[16]>(sv);
             float dt[16];                                // 1 - t^2 of the cap
             if constexpr ((MOD & (MOD_CAP | MOD_BIAS)) != 0)
-              bwd_score<MOD>(x, dt, p.sc, sl2, ysc, slope2, static_cast<float>(key - off - i * 128 - c0));
-            const float mul1 = (MOD & MOD_BIAS) ? 1.f : mul;   // with a bias its slope carries the NaN
+              bwd_score<MOD>(x, dt, mul, ysc, slope2, static_cast<float>(key - off - i * 128 - c0));
+            const float mul1 = (MOD & MOD_BIAS) ? 1.f : mul;   // with a bias bwd_score has taken it
             const uint32_t bits = m[sc >> 1] >> ((sc & 1) * 16);
 #pragma unroll
             for (int t4 = 0; t4 < 4; ++t4) {

@@ -269,34 +269,27 @@ __device__ __forceinline__ int fwd_key_doc(const FwdParams& p, int b, int j) {
 
 // Scored variants, one warp: clears the rows of a 128-row V tile (bf16, 128-byte
 // column blocks of 16 KB) that hold an inf or NaN and writes their bits to
-// bad[0..4).  One pass of x * 0 + a keeps a NaN once any x is not finite; only
-// then are the rows told apart.
+// bad[0..4).  One pass tells whether there are any; only then are the rows told
+// apart.
 template <int D>
 __device__ __forceinline__ void fwd_clean_v(uint8_t* tile, uint32_t* bad) {
   const int lane = threadIdx.x & 31;
   const uint4* t4 = reinterpret_cast<const uint4*>(tile);
   const __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
-  auto poison = [&](const uint4& w, __nv_bfloat162 a) {
-    a = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&w.x), zero, a);
-    a = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&w.y), zero, a);
-    a = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&w.z), zero, a);
-    return __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&w.w), zero, a);
-  };
-  auto is_nan = [](__nv_bfloat162 a) { return __hisnan(a.x) || __hisnan(a.y); };
   __nv_bfloat162 acc = zero, acc2 = zero;
 #pragma unroll 4
   for (int c = lane; c < 128 * D * 2 / 16; c += 64) {
-    acc = poison(t4[c], acc);
-    acc2 = poison(t4[c + 32], acc2);
+    acc = poison8(t4[c], acc);
+    acc2 = poison8(t4[c + 32], acc2);
   }
   uint32_t word = 0;
-  if (__any_sync(0xffffffffu, is_nan(acc) || is_nan(acc2))) {
+  if (__any_sync(0xffffffffu, is_nan2(acc) || is_nan2(acc2))) {
     for (int w = 0; w < 4; ++w) {
       uint4* row = reinterpret_cast<uint4*>(tile + (w * 32 + lane) * 128);
       __nv_bfloat162 a = zero;
       for (int kb = 0; kb < D / 64; ++kb)
-        for (int c = 0; c < 8; ++c) a = poison(row[kb * 1024 + c], a);
-      const bool b = is_nan(a);
+        for (int c = 0; c < 8; ++c) a = poison8(row[kb * 1024 + c], a);
+      const bool b = is_nan2(a);
       if (b)
         for (int kb = 0; kb < D / 64; ++kb)
           for (int c = 0; c < 8; ++c) row[kb * 1024 + c] = make_uint4(0u, 0u, 0u, 0u);

@@ -154,15 +154,16 @@ __device__ __forceinline__ void doc_bits(int id, const int (&other)[W], uint32_t
   for (int w = 0; w < W; ++w) m[w] &= d[w];
 }
 
-// No inf or NaN among eight bf16: x * 0 + a keeps a NaN once any x is not finite.
-__device__ __forceinline__ bool finite8(const uint4& w) {
+// Is there an inf or NaN among bf16 values?  x * 0 + a keeps a NaN once any x is
+// not finite.
+__device__ __forceinline__ __nv_bfloat162 poison8(const uint4& w, __nv_bfloat162 a) {
   const __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
-  __nv_bfloat162 a = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&w.x), zero);
+  a = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&w.x), zero, a);
   a = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&w.y), zero, a);
   a = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&w.z), zero, a);
-  a = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&w.w), zero, a);
-  return !__hisnan(a.x) && !__hisnan(a.y);
+  return __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&w.w), zero, a);
 }
+__device__ __forceinline__ bool is_nan2(__nv_bfloat162 a) { return __hisnan(a.x) || __hisnan(a.y); }
 
 // -------------------------------------------------------------------- cap --
 __device__ __forceinline__ float rcp_approx(float x) {
