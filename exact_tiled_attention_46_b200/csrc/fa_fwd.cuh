@@ -98,7 +98,8 @@ struct FwdCfg {  // scored variants: a two-entry item queue and the V tiles' sta
 // when it grows by more than FWD_TAU, O and the sums are rescaled in place, and
 // P is recomputed.
 constexpr float FWD_TAU = 8.0f;
-constexpr float FWD_CAP_FREE = 80.0f;   // caps (log2 units) up to which no largest score is looked for
+// Caps (log2 units; 50.6 in score units) up to which no largest score is looked for.
+constexpr float FWD_CAP_FREE = 73.0f, FWD_CAP_ROOM = 24.0f;
 constexpr int FWD_LAUNCH_REGS = 168;
 // With a cap the scores come 32 columns at a time and the softmax warps need
 // fewer registers, while the thread that issues the products gains from more
@@ -622,7 +623,7 @@ fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
     [[maybe_unused]] f2 cscale = 0, ctwo = 0, cy = 0, ck0 = 0, ck1 = 0, ck2 = 0, ck3 = 0, ck4 = 0, ck5 = 0;
     if constexpr (MOD != MOD_NONE && !(MOD & MOD_CAP)) cscale = f2_dup(sl2);
     if constexpr ((MOD & MOD_BIAS) != 0) ctwo = f2_dup(2.f);
-    [[maybe_unused]] const float ysc = p.sc.y_scale, cap2 = p.sc.cap_log2, m_base = fmaxf(cap2 - 60.f, 0.f);
+    [[maybe_unused]] const float ysc = p.sc.y_scale, cap2 = p.sc.cap_log2, m_base = fmaxf(cap2 - FWD_CAP_ROOM, 0.f);
     if constexpr (CAP) {
       cy = f2_dup(p.sc.y_scale);
       ck0 = f2_dup(FA_TANH_C0 * cap2);
@@ -712,11 +713,12 @@ fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
         if constexpr (CAP) {
           // ------------------------------------------------- capped scores --
           // The cap bounds every score, so the reference needs no search: it is
-          // cap2 - 60 (at least 0) less the bias of the nearest key seen so far,
-          // which keeps p below 2^60 and a row's largest p above 2^-100 for caps
-          // up to FWD_CAP_FREE (log2 units); beyond, and where the bias grows with
-          // the distance (a negative slope), the tile's largest score is looked
-          // for first.  Without a search no tile is exponentiated twice,
+          // cap2 - 24 (at least 0) less the bias of the nearest key seen so far,
+          // which keeps p below 2^24 (2^32 with a bias, whose reference follows
+          // FWD_TAU behind) and a row's largest p above 2^(24 - 2 cap2), 2^-122 at
+          // FWD_CAP_FREE: sums of 2^24 terms p v stay in fp32 for |v| < 2^64.  A
+          // larger cap, or a bias that grows with the distance (a negative slope):
+          // the tile's largest score is looked for first.  Without a search no tile is exponentiated twice,
           // so S can be read 32 columns at a time and the loop stay rolled: fully
           // unrolled, the polynomial's code outgrows the instruction cache.
           const int kb0 = fwd_tile<MOD>(I, j) * 128, pos = row + off;

@@ -281,9 +281,11 @@ fa_status fa_attn_merge(const float* o_a, const float* lse_a, const float* o_b, 
  * the row) let the kernels skip the key tiles of other documents.  The slopes
  * are constants: no gradient is formed for them.  With slopes, Lq and Lk must
  * stay below 2^24, where distances are exact in fp32, and scale must be at least
- * 2^-64 (else FA_ERR_UNSUPPORTED; |slope| below 2^60 stays finite).  With
- * a cap, |v| must stay below 2^40: probabilities are formed against a fixed
- * reference and reach 2^60 before O is normalised.
+ * 2^-64 (else FA_ERR_UNSUPPORTED; |slope| below 2^60 stays finite).  |v| must
+ * stay below 2^64: probabilities reach 2^32 (with a cap) before O is normalised,
+ * and O is summed in fp32.  With a cap c the largest one of a row whose every
+ * score lies at -c may be as small as 2^(24 - 2.9 c), and v below 2^-126 over
+ * that loses bits there; elsewhere v has its whole range down to 2^-78.
  */
 typedef struct {
   float softcap;

@@ -252,3 +252,24 @@ def test_keys_of_documents_in_any_order_that_no_query_has():
         assert torch.equal(got[1], ref[1]) and torch.equal(got[2], ref[2]) and same_sums(got[0], ref[0], 64.0)
         p.k, p.v = k, v
 
+
+
+# ------------------------------------------------------------ range of v --
+@pytest.mark.parametrize("cap,bias,boost", [(0.0, False, 1.0), (0.0, True, 8.0), (20.0, False, 8.0), (30.0, True, 8.0), (50.0, False, 16.0),
+                                            (50.0, True, 16.0), (50.6, False, 40.0), (55.0, False, 16.0), (70.0, True, 16.0)])
+def test_values_far_from_one(cap, bias, boost):
+    """V times a power of two gives O times that, to the bit upwards (p up to 2^32, 330 keys, |v| up to 2^78: below 2^127),
+    and within the bounds down to 2^-40."""
+    for sign in (1.0, -1.0):
+        p = S.Problem(1, 2, 1, 260, 330, 64, cap=cap, bias=bias, boost=boost, docs=(150, 0), seed=41)
+        p.k[:, :, :, 0], p.q[:, :, :, 0] = 4.0, sign * boost                      # scores towards one end of the cap
+        o, lse = forward(p, o_dtype=torch.float32)
+        S.check_fwd(p, o, lse, bf16_output=False)
+        v = p.v.clone()
+        p.v = v * 2.0 ** 75
+        big, _ = forward(p, o_dtype=torch.float32)
+        assert torch.equal(big, o * 2.0 ** 75)
+        p.v = v * 2.0 ** -40
+        if sign > 0 or not cap:
+            small, lse = forward(p, o_dtype=torch.float32)
+            S.check_fwd(p, small, lse, bf16_output=False)
