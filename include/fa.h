@@ -322,8 +322,9 @@ fa_status fa_fwd_scored(const void* q, const void* k, const void* v, void* o, vo
  * dO, o or its lse, and a key with one in k or v, get NaN gradients, and so do the
  * keys that such a query sees and the queries that see such a key; no others do.
  * The products run on fp16 operands as in fa_bwd: each tensor's largest finite
- * magnitude, of the rows that see or are seen by some other, sets its scale, and
- * values below 2^-22 of it lose bits.  workspace: at least
+ * magnitude, of the rows that see or are seen by some other, sets its scale, next
+ * to which very small elements lose bits (half a step: 2^-32 of that magnitude in
+ * q, k and v, 2^-23 in dO).  workspace: at least
  * fa_bwd_scored_workspace_size() bytes, 256-byte aligned.
  */
 size_t fa_bwd_scored_workspace_size(int B, int Hq, int Lq, int Lk, int D);
