@@ -1084,7 +1084,7 @@ fa_status fa_cache_evict(const fa_kv_rows* src, const fa_kv_rows* dst, const flo
   p.dst = fill(dst, rows[1]);
   p.w_src = weights_src; p.w_dst = weights_dst; p.len_src = seqlens_src; p.len_dst = seqlens_dst; p.kept = kept;
   p.B = B; p.Hkv = Hkv; p.D = D; p.keep = keep; p.recent = recent;
-  p.w_src_ld = weights_src_ld; p.w_dst_ld = weights_dst_ld; p.in_place = in_place;
+  p.w_src_ld = weights_src_ld; p.w_dst_ld = weights_dst_ld;
   const int sms = sm_count();
   if (sms <= 0) return FA_ERR_CUDA;
   // a slice is a power of two of 16-byte chunks: the whole row where blocks own

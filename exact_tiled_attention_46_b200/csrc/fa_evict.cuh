@@ -47,7 +47,6 @@ struct EvictParams {
   int B, Hkv, D, keep, recent, w_src_ld, w_dst_ld;
   int slice_chunks;        // 16-byte chunks of a row that one move block takes (a power of two)
   int cached;              // rows whose keys the select kernel keeps in shared memory
-  int in_place;
 };
 
 enum : uint32_t { W_EVICT_PAGE = 0x601, W_IDX_EVICT = 0x409 };

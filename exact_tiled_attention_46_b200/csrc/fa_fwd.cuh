@@ -62,7 +62,7 @@ struct FwdParams {
   void* o;                 // [B, Lq, Hq, D] bf16 or fp32
   float* lse;              // [B, Hq, Lq] or nullptr
   int B, Hq, Hkv, Lq, Lk;
-  int num_pairs;           // ceil(Lq / 256)
+  int num_pairs;           // items per (batch, head): ceil(Lq / 256), scored ceil(Lq / item_rows)
   float scale_log2;        // scale * log2(e) (e4m3 inputs: times the Q and K scales)
   float o_scale;           // multiplies O (e4m3 inputs: the V scale; else 1)
   int o_fp32;
@@ -574,16 +574,10 @@ fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUt
   } else if (MOD != MOD_NONE && warp == 11) {
     // ------------------------------------------------ V tiles seen in part --
     int it = 0;
-    bool ok = true;
-    [[maybe_unused]] bool more = true;
-    for (int r = 0; ok && (MOD != MOD_NONE ? more : r * G < num_items); ++r) {
+    bool ok = true, more = true;
+    for (int r = 0; ok && more; ++r) {
       int w;
-      if constexpr (MOD == MOD_NONE) {
-        w = fwd_item_index(r);
-        if (w >= num_items) continue;
-      } else if (!take(r, w, ok, more, true)) {
-        continue;
-      }
+      if (!take(r, w, ok, more, true)) continue;
       const FwdItem I = fwd_item<CAUSAL, MOD>(p, w);
       int kuni = I.n > 0 ? fwd_key_doc(p, I.b, I.j0) : -1;
       for (int jj = 0; jj < I.n; ++jj) {

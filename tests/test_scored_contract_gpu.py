@@ -273,3 +273,34 @@ def test_values_far_from_one(cap, bias, boost):
         if sign > 0 or not cap:
             small, lse = forward(p, o_dtype=torch.float32)
             S.check_fwd(p, small, lse, bf16_output=False)
+
+
+# ------------------------------------------------------------------ capture --
+def test_training_step_without_documents_captured():
+    """No kernel of documents' facts ahead: the chain begins with a memset. Two graphs, one workspace, replayed in turn."""
+    p, p2 = (S.Problem(2, 4, 2, 300, 300, 64, cap=9.0, bias=True, seed=s) for s in (61, 62))
+    B, Hq, Hkv, Lq, Lk, D = p.shape
+    q, k, v, do = cuda(p, "q", "k", "v", "do")
+    how = p.how("cuda")
+    ws = torch.empty(fa.bwd_scored_workspace_size(B, Hq, Lq, Lk, D), dtype=torch.uint8, device="cuda")
+
+    def step():
+        o, lse = fa.fwd_scored(q, k, v, **how)
+        return (o, lse) + fa.bwd_scored(q, k, v, o, do, lse, workspace=ws, grad_dtype=torch.float32, **how)
+
+    step()
+    graphs, outs = [], []
+    for _ in range(2):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            outs.append(step())
+    for src in (p2, p):
+        for a, b in zip((q, k, v, do), cuda(src, "q", "k", "v", "do")):
+            a.copy_(b)
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        for out in outs:
+            S.check_fwd(src, *out[:2])
+            S.check_bwd(src, *out[2:], bf16_output=False, fine=True)
+        assert torch.equal(outs[0][3], outs[1][3]) and torch.equal(outs[0][4], outs[1][4])
