@@ -43,8 +43,8 @@
 // cached row once the sequence's log-sum is known.  That costs 8 bytes per
 // score of traffic (3% of the cache's bytes at 4 heads of 128 dimensions each)
 // where a second pass over K would cost half of them again.  64 sequences of
-// 1024 to 32768 rows, 32 query and 8 kv heads of 128, with a cap: 764 us without
-// weights (4.83 GB of cache: 737 us at the copy rate), 862 with them.  One
+// 1024 to 32768 rows, 32 query and 8 kv heads of 128, with a cap: 750 us without
+// weights (4.83 GB of cache: 737 us at the copy rate), 840 with them.  One
 // sequence of 4000 rows: 8 us and 4 for the join, latency throughout.
 #pragma once
 #include "sm100.cuh"

@@ -35,16 +35,17 @@
 // item's rows sees in part, warp 11 looks for V rows that hold an inf or NaN
 // before the product reads them, clears them, and names them to the softmax
 // warps; a row that may see one of them ends as NaN, the others are untouched.
-// With no cap and no bias the scored kernel takes 107 us where the plain one
-// takes 84 (causal B4 H16 L2048 D128); without warp 11's code it takes 96, its
-// waits and looks alone cost nothing.  A cap adds 20 us (its polynomial), a bias
-// 4, MOD_FINE 25 (the second set of products and stores).  Floors there: 41 us of
-// products, 29 of exponentials; what bounds all of them is the chain from one S
-// through P to the next on two warps per sub-partition.
+// With nothing changed the scored kernel takes 104 us where the plain one takes
+// 86 (causal B4 H16 L2048 D128); without warp 11's code it takes 10 less, its
+// waits and looks alone cost nothing.  P in two parts adds 28 us (the second set
+// of products and stores), a cap 16 to that (its polynomial), a bias 7, o_lo 7
+// (2 with a cap).  Floors there: 41 us of products (62 in two parts), 29 of
+// exponentials; what bounds all of them is the chain from one S through P to the
+// next on two warps per sub-partition.
 // MOD_FINE keeps P in two bf16 parts (the second takes the other half of S's
 // columns and a second set of P.V products), so that O is off by its own rounding
-// alone: relative error 1.66e-3 in bf16 where one part gives 1.9e-3, for 158 us
-// instead of 128 (cap, B4 H16 L2048 D128) and 901 instead of 661 (bias and prefix,
+// alone: relative error 1.66e-3 in bf16 where one part gives 1.9e-3, for 157 us
+// instead of 128 (cap, B4 H16 L2048 D128) and 900 instead of 661 (bias and prefix,
 // Hq32 Hkv8 L8191 D128).  Every scored call takes it but the one that changes
 // nothing, which is fa_fwd_ex bit for bit.  With o_lo it writes, beside the bf16 O,
 // what that rounding took off: the gradient's Delta = dO.O subtracts from dP
@@ -103,9 +104,9 @@ constexpr float FWD_CAP_FREE = 73.0f, FWD_CAP_ROOM = 24.0f;
 constexpr int FWD_LAUNCH_REGS = 168;
 // With a cap the scores come 32 columns at a time and the softmax warps need
 // fewer registers, while the thread that issues the products gains from more
-// (capped prefill B4 H16 L2048 D128: 129 us with 208 and 88, 133 with 224 and
-// 56, 134 with 192 and 120; Hq32 Hkv8 L8192: 758, 811, 822); the other variants
-// hold a whole row of S and spill below 224 (a bias: 111 us, 113 with 208).
+// (capped prefill B4 H16 L2048 D128: 149 us with 208 and 88, 152 with 224 and
+// 56, 154 with 192 and 120; Hq32 Hkv8 L8192: 940, 940, 963); the other variants
+// hold a whole row of S and spill below 224 (a bias: 140 us, 142 with 208).
 template <int MOD>
 struct FwdRegs {
   static constexpr int SOFTMAX = (MOD & MOD_CAP) ? 208 : 224, CTRL = (MOD & MOD_CAP) ? 88 : 56;

@@ -42,7 +42,7 @@ __device__ __forceinline__ int score_prefix(const ScoreParams& s, int b, int Lk)
 // overlap that interval (exact for packed documents, which only grow along the
 // row; for ids in any order the range may hold tiles without a common document,
 // and the element masks decide).  Reads 4 (Lq + Lk) bytes per block out of L2:
-// 3 us at L = 1000, 7 at B8 L4096 (of a forward of 425), hidden in part by the
+// 3 us at L = 1000, 9 at B8 L4096 (of a forward of 500), hidden in part by the
 // next kernel's start.  `unseen` (or nullptr) receives 128 bits per key tile: the
 // keys that no query may see.  A warp looks its 32 keys up among the range's
 // queries, 32 at a time from the first that position allows, until all are found

@@ -10,9 +10,9 @@
 // Floor: 2 D FLOP and one exponential per pair.  The MUFU unit (16 exponentials
 // per clock and SM, 1024 cycles for a 128 x 128 tile) bounds it before the
 // tensor core does (512 cycles at D = 128).  Measured: a causal prompt of 4095
-// tokens, 32 query and 8 kv heads of D = 128, 104 us (its exponentials alone:
+// tokens, 32 query and 8 kv heads of D = 128, 101 us (its exponentials alone:
 // 58 us; the MUFU unit is 71% busy while an SM has work); the last 64 queries of
-// 4 prompts over 8192 keys with a cap, 62 us (an item then holds four pairs of
+// 4 prompts over 8192 keys with a cap, 58 us (an item then holds four pairs of
 // half-empty tiles, and what a pair costs besides its exponentials counts).
 // Four neighbouring key tiles per item, one per warpgroup, so that no sums are
 // joined and a Q tile is read once for the four, measured 120 and 73 us: the
