@@ -52,24 +52,24 @@ NOMINAL_PEAKS = {"bf16_tflops": 2250.0, "hbm_gbs": 8000.0,
 # its units of work (see the profiles/ summaries for the captured case).
 PROFILED_TRAFFIC = {
     "fwd_kernel causal_prefill": {"sources": ("csrc/fa_fwd.cuh", "csrc/sm100.cuh"),
-                                  "sha256_16": "1d2d7cd6a4be41b9", "bytes": 128716800 + 9652224},
+                                  "sha256_16": "f25721509ed8c2a9", "bytes": 132005632 + 10423552},
     "fwd_kernel long_gqa_prefill": {"sources": ("csrc/fa_fwd.cuh", "csrc/sm100.cuh"),
-                                    "sha256_16": "1d2d7cd6a4be41b9", "bytes": 350520576 + 97943552},
+                                    "sha256_16": "f25721509ed8c2a9", "bytes": 343002368 + 99009024},
     "fwd_kernel<fp8> causal_prefill": {"sources": ("csrc/fa_fwd.cuh", "csrc/sm100.cuh"),
-                                       "sha256_16": "1d2d7cd6a4be41b9", "bytes": 50423040 + 2916096},
+                                       "sha256_16": "f25721509ed8c2a9", "bytes": 50431232 + 2622208},
     "bwd_main_kernel train_fwd_bwd": {"sources": ("csrc/fa_bwd.cuh", "csrc/sm100.cuh"),
-                                      "sha256_16": "5c857fe2ae613f5d", "bytes": 406924032 + 223591936},
+                                      "sha256_16": "34a218266210f5bb", "bytes": 406988288 + 225958656},
     # captured on the first 16 sequences of the decode workload (1.35888 GB of KV
     # rows), scaled to a launch by the KV bytes it reads
     "decode_split_kernel splitkv_decode": {"sources": ("csrc/fa_decode.cuh", "csrc/sm100.cuh"),
-                                           "sha256_16": "5ded7d6af4217d21",
-                                           "bytes_per_kv_byte": (1362382592 + 13402112) / 1358876672},
+                                           "sha256_16": "167b3357f9e43c2c",
+                                           "bytes_per_kv_byte": (1362386688 + 13195776) / 1358876672},
     "decode_split_kernel<append> splitkv_decode": {"sources": ("csrc/fa_decode.cuh", "csrc/sm100.cuh"),
-                                                   "sha256_16": "5ded7d6af4217d21",
-                                                   "bytes_per_kv_byte": (1366725632 + 19940096) / 1358876672},
+                                                   "sha256_16": "167b3357f9e43c2c",
+                                                   "bytes_per_kv_byte": (1366697472 + 19513856) / 1358876672},
     "decode_split_kernel<paged16> splitkv_decode": {"sources": ("csrc/fa_decode.cuh", "csrc/sm100.cuh"),
-                                                    "sha256_16": "5ded7d6af4217d21",
-                                                    "bytes_per_kv_byte": (1362172928 + 13146368) / 1358876672},
+                                                    "sha256_16": "167b3357f9e43c2c",
+                                                    "bytes_per_kv_byte": (1362198784 + 13215232) / 1358876672},
 }
 
 
