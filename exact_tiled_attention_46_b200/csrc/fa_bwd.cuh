@@ -64,13 +64,15 @@
 // that no query sees take part as zeros, whatever their memory holds, and count
 // for none of the input maxima.
 // An inf or NaN stays with the pairs that it belongs to, though 0 * NaN is NaN in
-// the products: inf and NaN are left out of the maxima and enter the products as
-// zeros; a query row that holds one (in q, dO, Delta or LSE) gets LSE = NaN
-// instead, and the thread of a key that does (in K or V) takes a NaN for a factor
-// of its scores, so that P and dS are NaN for its allowed pairs and 0 for the others
-// (647 us above, 617 without).
+// the products: inf, NaN and magnitudes from 2^75 on are left out of the maxima,
+// and what is then not finite in fp16 enters the products as zeros; a query row
+// that holds such a value (in q, dO, Delta or LSE) gets LSE = NaN instead, and the
+// thread of a key that does (in K or V) takes a NaN for a factor of its scores, so
+// that P and dS are NaN for its allowed pairs and 0 for the others (647 us above,
+// 617 without).
 #pragma once
 #include "sm100.cuh"
+#include <cuda_fp16.h>
 #include "fa_score.cuh"
 #include "fa.h"
 
@@ -87,6 +89,13 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
+}
+
+// NaN once any of eight fp16 values is not finite: x * 0 + a.
+__device__ __forceinline__ __half2 poison8h(const uint32_t (&h)[4], __half2 a) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) a = __hfma2(*reinterpret_cast<const __half2*>(&h[e]), __float2half2_rn(0.f), a);
+  return a;
 }
 
 template <int D>
@@ -215,15 +224,16 @@ __device__ __forceinline__ BwdScales bwd_scales(const uint32_t* amax, int D) {
 
 // Largest |x| of q, k, v, dO (bf16) into amax[0..3] (float bits; zeroed
 // before).  blockIdx.y picks the tensor; one atomic per block.  FINITE: of the
-// finite values; |x| + 0x80 carries an inf's or NaN's exponent past its 15 bits,
-// so that it ends below every finite one.
+// values below 2^75, where the scales end; adding BWD_TOP_GAP to |x|'s 15 bits
+// carries a larger one, an inf or a NaN past them, so that it ends below all others.
+constexpr uint32_t BWD_TOP_GAP = 0x8000u - ((127u + 75u) << 7);
 template <bool FINITE>
 __device__ __forceinline__ uint32_t bwd_top(const uint4& w) {
   const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
   uint32_t m = 0;
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    if constexpr (FINITE) m = __vmaxu2(m, ((ws[e] & 0x7fff7fffu) + 0x00800080u) & 0x7fff7fffu);
+    if constexpr (FINITE) m = __vmaxu2(m, ((ws[e] & 0x7fff7fffu) + BWD_TOP_GAP * 0x10001u) & 0x7fff7fffu);
     else m = max(m, max(ws[e] & 0x7fffu, (ws[e] >> 16) & 0x7fffu));
   }
   return FINITE ? max(m & 0xffffu, m >> 16) : m;
@@ -253,7 +263,7 @@ __global__ void __launch_bounds__(256) bwd_amax_kernel(const uint16_t* q, const 
   __syncthreads();
   if (threadIdx.x == 0) {
     for (int w = 1; w < static_cast<int>(blockDim.x >> 5); ++w) m = max(m, wmax[w]);
-    if (FINITE) m = m >= 0x80u ? m - 0x80u : 0u;
+    if (FINITE) m = m >= BWD_TOP_GAP ? m - BWD_TOP_GAP : 0u;
     if (m != 0) atomicMax(&amax[t], m << 16);      // |x| as float bits
   }
 }
@@ -312,7 +322,7 @@ __global__ void __launch_bounds__(256) bwd_amax_scored_kernel(const uint16_t* q,
   __syncthreads();
   if (threadIdx.x == 0) {
     for (int w = 1; w < 8; ++w) m = max(m, wmax[w]);
-    m = m >= 0x80u ? m - 0x80u : 0u;
+    m = m >= BWD_TOP_GAP ? m - BWD_TOP_GAP : 0u;
     if (m != 0) atomicMax(&amax[t], m << 16);      // |x| as float bits
   }
 }
@@ -379,7 +389,10 @@ __global__ void __launch_bounds__(256) bwd_pre_kernel(const uint16_t* o, const u
         hd[e] = pack_f16x2(g0 * fdo, g1 * fdo);
         hq[e] = pack_f16x2(__uint_as_float(xv[e] << 16) * fq, __uint_as_float(xv[e] & 0xffff0000u) * fq);
       }
-      if (SCORED && is_nan2(poison8(x, poison8(g, __float2bfloat162_rn(0.f))))) acc = __int_as_float(0x7fffffff);
+      if constexpr (SCORED) {
+        const __half2 bad = poison8h(hq, poison8h(hd, __float2half2_rn(0.f)));
+        if (__hisnan(bad.x) || __hisnan(bad.y)) acc = __int_as_float(0x7fffffff);
+      }
       if (SCORED) {                                // the dQ accumulator, zeroed here instead of by a launch of its own
         const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
         reinterpret_cast<float4*>(zero_acc)[2 * off] = z;
@@ -753,23 +766,23 @@ bwd_main_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         const float fk = bwd_pow2(sc_in.kk), fv = bwd_pow2(sc_in.kv);
         uint4* kv4 = reinterpret_cast<uint4*>(smem + u * 2 * C::TILE + C::K_OFF);   // K then V, contiguous
         constexpr int N16 = 2 * C::TILE / 16;
-        [[maybe_unused]] __nv_bfloat162 acc = __float2bfloat162_rn(0.f);
+        [[maybe_unused]] __half2 acc = __float2half2_rn(0.f);
 #pragma unroll 4
         for (int c = threadIdx.x; c < N16; c += 256) {
           const float f = (c < C::TILE / 16) ? fk : fv;
           const uint4 w = kv4[c];
-          if constexpr (MOD != MOD_NONE) acc = poison8(w, acc);
           const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
           uint32_t hs[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             hs[e] = pack_f16x2(__uint_as_float(ws[e] << 16) * f, __uint_as_float(ws[e] & 0xffff0000u) * f);
+          if constexpr (MOD != MOD_NONE) acc = poison8h(hs, acc);
           kv4[c] = make_uint4(hs[0], hs[1], hs[2], hs[3]);
         }
         if constexpr (MOD != MOD_NONE) {
           // seldom: zeros for the keys that no query sees and for what is not
-          // finite (the scales keep every finite value finite in fp16)
-          if (I.kmiss || is_nan2(acc)) {
+          // finite in fp16 (besides inf and NaN: magnitudes left out of the maxima)
+          if (I.kmiss || __hisnan(acc.x) || __hisnan(acc.y)) {
             const uint32_t* miss = p.unseen + (static_cast<size_t>(I.b) * ((p.Lk + 127) >> 7) + I.j) * 4;
             for (int c = threadIdx.x; c < N16; c += 256) {
               const int kr = ((c * 16) & 16383) / 128;   // row of the tile

@@ -321,6 +321,7 @@ fa_status fa_fwd_scored(const void* q, const void* k, const void* v, void* o, vo
  * The tanh's derivative is part of dq and dk.  A query with an inf or NaN in q,
  * dO, o or its lse, and a key with one in k or v, get NaN gradients, and so do the
  * keys that such a query sees and the queries that see such a key; no others do.
+ * (Magnitudes of 2^75 and more may count as infinite.)
  * The products run on fp16 operands as in fa_bwd: each tensor's largest finite
  * magnitude, of the rows that see or are seen by some other, sets its scale, next
  * to which very small elements lose bits (half a step: 2^-32 of that magnitude in

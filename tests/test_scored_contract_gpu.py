@@ -304,3 +304,22 @@ def test_training_step_without_documents_captured():
             S.check_fwd(src, *out[:2])
             S.check_bwd(src, *out[2:], bf16_output=False, fine=True)
         assert torch.equal(outs[0][3], outs[1][3]) and torch.equal(outs[0][4], outs[1][4])
+
+
+# -------------------------------------------------------------- huge numbers --
+@pytest.mark.parametrize("which", ("q", "k", "v", "do"))
+@pytest.mark.parametrize("name", ("docs", "docs_cap", "docs_not_causal"))
+def test_gradient_beside_a_document_of_huge_numbers(name, which):
+    """Finite, and far past the range that the fp16 scales reach: the other documents' gradients keep their bits."""
+    c = dict(NEIGHBOURS[name])
+    p = S.Problem(*c.pop("shape"), seed=71, **c)
+    x = getattr(p, which)
+    hit = p.docs[1][0] == p.docs[1][0, 150]
+    x[0, hit] = 0.0
+    _, _, ref = gradients(p)
+    x[0, hit] = 3e38
+    _, _, got = gradients(p)
+    keep = ~hit.cuda()
+    for g, r in zip(got[1:], ref[1:]):
+        assert torch.equal(g[1], r[1]) and torch.equal(g[0, keep], r[0, keep])
+    assert same_sums(got[0][1], ref[0][1], 64.0) and same_sums(got[0][0, keep], ref[0][0, keep], 64.0)
