@@ -78,6 +78,13 @@ def test_bwd_workspace_is_checked_to_the_byte(L):
     assert L.fa_bwd_scored(*dict(BWD, nbytes=need - 1).values()) == BAD
 
 
+def test_bwd_workspace_holds_the_keys_that_no_query_sees():
+    """128 bits per key tile beside the tile facts, which other calls do without."""
+    for B, Lk in ((1, 8), (3, 129), (2, 5000)):
+        extra = fa.bwd_scored_workspace_size(B, 2, 64, Lk, 64) - fa.bwd_workspace_size(B, 2, 64, 64) - fa.scored_workspace_size(B, 64, Lk)
+        assert extra >= B * -(-Lk // 128) * 16 and extra % 256 == 0
+
+
 DEC = dict(q=P, k_new=None, v_new=None, k=P, v=P, table=None, lens=P, starts=None, o=P, lse=None, weights=None, ld=0, B=2,
            Hq=4, Hkv=2, num=2, page=100, pps=1, D=64, scale=0.1, softcap=0.0, slopes=None, o_dtype=0, ws=P, nbytes=0,
            stream=None)
